@@ -431,6 +431,205 @@ bnn_status bnn_dense_binact_f32(const uint32_t* Xp, int64_t ldXp,
                                 int64_t M, int64_t N, int64_t K,
                                 float* Y, int64_t ldY, bnn_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The decoder's key/value cache and what runs over it.
+ *
+ * Between the QKV projection and the output projection of a decoder whose
+ * linear layers are the 1-bit ones above ([P5] "BitNet: 1-bit Transformer":
+ * binary or ternary projections; [P3]: the rest of the block stays higher
+ * precision), four calls work on one paged cache, all driven by device data
+ * only, so a step of them can be captured in a HIP graph:
+ *   bnn_qk_norm_rope     norm + rotate queries and keys, append keys, values
+ *   bnn_tree_attention   attention of the new tokens over the cache
+ *   bnn_cache_score_add  attention weight each cached token received, summed
+ *   bnn_cache_evict      drop rejected drafts, cut the cache to a budget
+ *
+ * Sequence b holds ctx[b] committed tokens in its slots 0 .. ctx[b]-1.  Its
+ * new tokens of a step (one for plain decoding; a tree or a run of drafted
+ * tokens; a chunk of a prompt) are T_b = indptr[b+1] - indptr[b] rows of the
+ * token tensors and take the slots ctx[b] .. ctx[b]+T_b-1.  Slots are in no
+ * order of position: attention does not need one, and bnn_cache_evict
+ * leaves none.
+ * ---------------------------------------------------------------------- */
+#define BNN_BF16 1
+#define BNN_F16  2
+#define BNN_F32  3
+
+/* A paged cache.  Host struct; K, V and table are device memory.  The row of
+ * slot s of sequence b, head h is dim elements at
+ *   K + page * k_page + (s % page_size) * k_slot + h * k_head,
+ *   page = table[b * ld_table + s / page_size]   (table NULL: page = b)
+ * and likewise for V.  Strides are in elements, multiples of 8, up to 2^47;
+ * K and V are 16-byte aligned; rows must not overlap.  dim: 64, 96, 128 or
+ * 256.  page_size is any number >= 1, up to 2^30.  A sequence has room for
+ * capacity = ld_table * page_size slots (page_size with table NULL), at most
+ * 2^30; tokens past it are neither written nor read.  A table entry outside
+ * 0 .. num_pages-1 names no page: nothing is written there, and its slots
+ * read as rows of zeros. */
+typedef struct bnn_kv_cache {
+    void* K; int64_t k_page, k_slot, k_head;
+    void* V; int64_t v_page, v_slot, v_head;
+    const int32_t* table; int64_t ld_table;  /* [B, ld_table] or NULL          */
+    int64_t num_pages, page_size;
+    int64_t kv_heads, dim;
+    int32_t dtype;                           /* BNN_BF16 or BNN_F16            */
+} bnn_kv_cache;
+
+/* The new tokens of a step.  Host struct; indptr and ctx are device memory.
+ * indptr must not decrease and start at 0; rows past indptr[B] are left alone
+ * (a buffer may be longer than the step).  max_nodes and max_ctx bound T_b
+ * and ctx[b] from above; they size grids and workspaces.  New tokens past
+ * max_nodes of a sequence get no output (and no cache slot from
+ * bnn_qk_norm_rope needs them: it goes by rows); a ctx[b] above max_ctx only
+ * costs speed.  A negative ctx[b] counts as 0. */
+typedef struct bnn_kv_batch {
+    const int32_t* indptr;                   /* [B + 1]                        */
+    const int32_t* ctx;                      /* [B]                            */
+    int64_t B, rows;                         /* rows: of the token tensors     */
+    int64_t max_nodes, max_ctx;
+} bnn_kv_batch;
+
+/* Arguments of bnn_qk_norm_rope.  Host struct, device pointers. */
+typedef struct bnn_rope_args {
+    const void* q; int64_t q_row, q_head;    /* [rows, heads, dim], strides in elements */
+    const void* k; int64_t k_row, k_head;    /* [rows, kv_heads, dim]          */
+    const void* v; int64_t v_row, v_head;
+    int32_t src_dtype;                       /* of q, k, v: BNN_F32, or the cache's dtype */
+    int64_t heads;
+    void* q_out; int64_t qo_row, qo_head;    /* [rows, heads, dim], the cache's dtype */
+    const int32_t* positions;                /* [rows]                         */
+    const float* turns; int64_t max_pos, rot;/* [max_pos, rot]: rot/2 cosines, then rot/2 sines */
+    int32_t interleaved;                     /* pairs (2i, 2i+1); 0: (i, i + rot/2) */
+    const float* q_weight; const float* k_weight; /* [dim] fp32, or NULL: no norm */
+    float eps;
+    int32_t* pos; float* score;              /* [B, kv_heads, ld_slots] or NULL */
+    int64_t ld_slots;
+} bnn_rope_args;
+
+/* For every new token and head: the RMS norm of the query and key heads (with
+ * its weight), the rotation of their first rot dimensions by the token's
+ * position, and the append of key and value to the cache, in one pass:
+ *     y = x * rsqrt(mean(x^2) + eps) * weight          (weight NULL: y = x)
+ *     (a, b) -> (a c - b s, b c + a s)   for each pair, c, s from turns[position]
+ * in fp32, rounded once to the cache's 16-bit type.  The token's slot also
+ * gets pos[b, h, slot] = its position and score[b, h, slot] = 0 where those
+ * are given.  rot is a multiple of 8, 0 .. dim.  Strides of q, k, v and their
+ * addresses are multiples of 4 elements, those of q_out of 8.  A token whose
+ * position is outside 0 .. max_pos-1 gets NaN in its rotated dimensions. */
+bnn_status bnn_qk_norm_rope(const bnn_kv_cache* cache, const bnn_kv_batch* batch,
+                            const bnn_rope_args* args, bnn_stream_t stream);
+
+/* Kinds of position scaling of bnn_rope_turns_host. */
+#define BNN_ROPE_PLAIN  0  /* theta_i = base^(-2i/rot)                                   */
+#define BNN_ROPE_LINEAR 1  /* theta_i / factor                                           */
+#define BNN_ROPE_BASE   2  /* base * factor^(rot/(rot-2)) in place of base               */
+#define BNN_ROPE_RAMP   3  /* by turns over the first context: theta_i kept for pairs that
+                              turn more than beta_fast times in old_ctx, theta_i / factor
+                              for those below beta_slow, a linear ramp over the pair index
+                              between; cosines and sines times 0.1 ln(factor) + 1        */
+#define BNN_ROPE_BANDS  4  /* by wavelength: theta_i kept where it turns more than
+                              beta_fast times in old_ctx, / factor below beta_slow times,
+                              and a blend linear in the number of turns between          */
+
+/* The table of bnn_qk_norm_rope in HOST memory: turns[p, i] = cos(p theta_i),
+ * turns[p, rot/2 + i] = sin(p theta_i) for p < max_pos, computed in double and
+ * rounded once.  rot: even, >= 2; base > 1; factor >= 1; RAMP and BANDS need
+ * old_ctx > 0 and beta_fast > beta_slow > 0.  Synchronous.
+ * Errors: NULL -> BNN_ERR_NULL; sizes -> BNN_ERR_SHAPE; the rest ->
+ * BNN_ERR_UNSUPPORTED. */
+bnn_status bnn_rope_turns_host(int64_t max_pos, int64_t rot, double base, int32_t kind, double factor,
+                               double old_ctx, double beta_fast, double beta_slow, float* turns);
+
+/* The packed visibility rows of a tree in HOST memory: bit j of row i is 1
+ * where node j is node i or one of its ancestors.  parent[i] < i, or -1 for a
+ * child of the last committed token.  mask [T, ld], ld >= ceil(T/32); all ld
+ * words are written.  Synchronous. */
+bnn_status bnn_tree_mask_host(const int32_t* parent, int64_t T, uint32_t* mask, int64_t ld);
+
+/* Arguments of bnn_tree_attention.  Host struct, device pointers. */
+typedef struct bnn_attn_args {
+    const void* q; int64_t q_row, q_head;    /* [rows, heads, dim], the cache's dtype,
+                                                16-byte aligned, strides multiples of 8 */
+    int64_t heads;                           /* a multiple of kv_heads; query head h reads
+                                                key head h / (heads / kv_heads)         */
+    const uint32_t* mask; int64_t ld_mask;   /* [rows, ld_mask] packed: bit j of a row = it
+                                                sees new token j of its sequence; tokens past
+                                                32 ld_mask are not seen.  NULL: tokens 0 .. its own */
+    float scale;
+    void* out; int64_t o_row, o_head;        /* [rows, heads, dim]; 16-byte aligned,
+                                                strides multiples of 8          */
+    int32_t out_dtype;                       /* BNN_F32 or the cache's dtype    */
+    float* lse; int64_t ld_lse;              /* [rows, ld_lse >= heads] or NULL */
+    void* workspace; int64_t workspace_bytes;/* bnn_tree_attention_workspace bytes,
+                                                16-byte aligned                 */
+} bnn_attn_args;
+
+/* Attention of every new token over its sequence's committed tokens and the
+ * new tokens that its mask row shows:
+ *     s_j = scale <q, k_j>;  lse = ln sum_j exp(s_j);  out = sum_j exp(s_j - lse) v_j
+ * with products and sums in fp32.  A row that sees nothing gives 0 and
+ * lse = -inf.  Values of unseen tokens do not matter, NaN and infinities
+ * included.  With a 16-bit out the weights are rounded to that type for the
+ * product with V; with fp32 out they keep 22 bits or more.  The workspace's
+ * contents need not be kept or cleared between calls. */
+bnn_status bnn_tree_attention(const bnn_kv_cache* cache, const bnn_kv_batch* batch,
+                              const bnn_attn_args* args, bnn_stream_t stream);
+
+/* Workspace bytes of bnn_tree_attention (0 where it needs none); -1 for
+ * arguments that it would refuse.  Device pointers are not looked at. */
+int64_t bnn_tree_attention_workspace(const bnn_kv_cache* cache, const bnn_kv_batch* batch, int64_t heads);
+
+/* Arguments of bnn_cache_score_add.  Host struct, device pointers. */
+typedef struct bnn_score_args {
+    const void* q; int64_t q_row, q_head;    /* as in bnn_attn_args             */
+    int64_t heads;
+    const float* lse; int64_t ld_lse;        /* [rows, ld_lse]: of the same attention */
+    const uint32_t* mask; int64_t ld_mask;   /* as in bnn_attn_args             */
+    const uint32_t* accept; int64_t ld_accept; /* [B, ld_accept] packed: bit i = new token i of
+                                                the sequence counts (past 32 ld_accept: does
+                                                not).  NULL: all count          */
+    float scale;
+    const float* score_in; float* score_out; /* [B, kv_heads, ld_slots]; may be the same */
+    int64_t ld_slots;
+} bnn_score_args;
+
+/* Adds to each slot's running sum the attention weight it received from the
+ * accepted new tokens and the query heads that share its key head:
+ *     score_out[b,h,j] = score_in[b,h,j] + sum_i sum_g exp(scale <q_ig, k_j> - lse_ig)
+ * over accepted i that see j, for the slots j < ctx[b] + T_b; entries of later
+ * slots are copied.  Each sum is taken in a fixed order in fp32: the same on
+ * every run. */
+bnn_status bnn_cache_score_add(const bnn_kv_cache* cache, const bnn_kv_batch* batch,
+                               const bnn_score_args* args, bnn_stream_t stream);
+
+/* Arguments of bnn_cache_evict.  Host struct, device pointers. */
+typedef struct bnn_evict_args {
+    const uint32_t* accept; int64_t ld_accept; /* as in bnn_score_args          */
+    int64_t budget;                          /* tokens kept per sequence at most, >= 0 */
+    int64_t recent;                          /* positions that are kept before others, >= 0 */
+    const int32_t* pos_in; int32_t* pos_out; /* [B, kv_heads, ld_slots]; may be the same */
+    const float* score_in; float* score_out; /* [B, kv_heads, ld_slots]; may be the same */
+    int64_t ld_slots;
+    int32_t* ctx_out;                        /* [B]; may be batch->ctx          */
+    void* workspace; int64_t workspace_bytes;/* bnn_cache_evict_workspace bytes, 16-byte aligned */
+} bnn_evict_args;
+
+/* Drops the new tokens that were not accepted, then cuts each sequence to
+ * keep = min(budget, what is left) tokens, for each key head its own choice:
+ * first the tokens whose position exceeds the highest one left minus recent,
+ * then by score, the highest first; equal scores by slot, the lowest first; a
+ * NaN score counts as -inf.  In place: tokens kept in slots below keep stay;
+ * the others, in order, fill the slots below keep that became free, in
+ * order.  K, V, pos and score move alike; the freed slots up to the old
+ * length get pos -1 and score 0, and ctx_out[b] = keep.  Calling it again
+ * on the same inputs (with other outputs than inputs) gives the same result. */
+bnn_status bnn_cache_evict(const bnn_kv_cache* cache, const bnn_kv_batch* batch,
+                           const bnn_evict_args* args, bnn_stream_t stream);
+
+/* Workspace bytes of bnn_cache_evict for B sequences of this cache; -1 for
+ * arguments that it would refuse. */
+int64_t bnn_cache_evict_workspace(const bnn_kv_cache* cache, int64_t B);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,6 +27,8 @@ __all__ = [
     "EPI_THRESH_PACK", "EPI_ALPHA_TENSOR", "EPI_BIAS_F32", "LIB_PATH",
     "weight_scale_tensor", "weight_scale_tensor_noalloc", "NOALLOC_MAX_ROWS", "quantize_act_i8", "pack_act_i8", "bwn_i8_linear", "MAX_K_I8", "bwn_f16_gemv", "MAX_K_F16",
     "W_TERNARY", "pack_weights_ternary", "EPI_SIGN_PACK", "pack_activations_rsign", "conv3x3_fused",
+    "KVCache", "qk_norm_rope", "rope_turns", "tree_mask", "tree_attention", "tree_attention_workspace",
+    "cache_score_add", "cache_evict", "cache_evict_workspace",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbnn.so")
@@ -93,6 +95,81 @@ class _I8Args(ctypes.Structure):
     ]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [
+        ("K", ctypes.c_void_p), ("k_page", ctypes.c_int64), ("k_slot", ctypes.c_int64), ("k_head", ctypes.c_int64),
+        ("V", ctypes.c_void_p), ("v_page", ctypes.c_int64), ("v_slot", ctypes.c_int64), ("v_head", ctypes.c_int64),
+        ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
+        ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+        ("kv_heads", ctypes.c_int64), ("dim", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class _KvBatch(ctypes.Structure):
+    _fields_ = [
+        ("indptr", ctypes.c_void_p), ("ctx", ctypes.c_void_p),
+        ("B", ctypes.c_int64), ("rows", ctypes.c_int64),
+        ("max_nodes", ctypes.c_int64), ("max_ctx", ctypes.c_int64),
+    ]
+
+
+class _RopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+        ("k", ctypes.c_void_p), ("k_row", ctypes.c_int64), ("k_head", ctypes.c_int64),
+        ("v", ctypes.c_void_p), ("v_row", ctypes.c_int64), ("v_head", ctypes.c_int64),
+        ("src_dtype", ctypes.c_int32),
+        ("heads", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p), ("qo_row", ctypes.c_int64), ("qo_head", ctypes.c_int64),
+        ("positions", ctypes.c_void_p),
+        ("turns", ctypes.c_void_p), ("max_pos", ctypes.c_int64), ("rot", ctypes.c_int64),
+        ("interleaved", ctypes.c_int32),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("pos", ctypes.c_void_p), ("score", ctypes.c_void_p),
+        ("ld_slots", ctypes.c_int64),
+    ]
+
+
+class _AttnArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+        ("mask", ctypes.c_void_p), ("ld_mask", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("out", ctypes.c_void_p), ("o_row", ctypes.c_int64), ("o_head", ctypes.c_int64),
+        ("out_dtype", ctypes.c_int32),
+        ("lse", ctypes.c_void_p), ("ld_lse", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
+class _ScoreArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+        ("lse", ctypes.c_void_p), ("ld_lse", ctypes.c_int64),
+        ("mask", ctypes.c_void_p), ("ld_mask", ctypes.c_int64),
+        ("accept", ctypes.c_void_p), ("ld_accept", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("score_in", ctypes.c_void_p), ("score_out", ctypes.c_void_p),
+        ("ld_slots", ctypes.c_int64),
+    ]
+
+
+class _EvictArgs(ctypes.Structure):
+    _fields_ = [
+        ("accept", ctypes.c_void_p), ("ld_accept", ctypes.c_int64),
+        ("budget", ctypes.c_int64), ("recent", ctypes.c_int64),
+        ("pos_in", ctypes.c_void_p), ("pos_out", ctypes.c_void_p),
+        ("score_in", ctypes.c_void_p), ("score_out", ctypes.c_void_p),
+        ("ld_slots", ctypes.c_int64),
+        ("ctx_out", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 _lib = None
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
@@ -129,11 +206,22 @@ def lib() -> ctypes.CDLL:
             "bnn_pack_weights_ternary": [_vp, _i64, _i64, _i64, _vp, ctypes.c_float, _vp, _vp, _i64, _vp, _vp],
             "bnn_pack_activations_rsign": [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp],
             "bnn_conv3x3_fused": [ctypes.POINTER(_FusedArgs), ctypes.POINTER(_ConvGeom), _vp],
+            "bnn_qk_norm_rope": [_vp, _vp, _vp, _vp],
+            "bnn_rope_turns_host": [_i64, _i64, ctypes.c_double, ctypes.c_int32, ctypes.c_double, ctypes.c_double,
+                                    ctypes.c_double, ctypes.c_double, _vp],
+            "bnn_tree_mask_host": [_vp, _i64, _vp, _i64],
+            "bnn_tree_attention": [_vp, _vp, _vp, _vp],
+            "bnn_cache_score_add": [_vp, _vp, _vp, _vp],
+            "bnn_cache_evict": [_vp, _vp, _vp, _vp],
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
+        L.bnn_tree_attention_workspace.argtypes = [_vp, _vp, _i64]
+        L.bnn_tree_attention_workspace.restype = _i64
+        L.bnn_cache_evict_workspace.argtypes = [_vp, _i64]
+        L.bnn_cache_evict_workspace.restype = _i64
         _lib = L
     return _lib
 
@@ -529,3 +617,299 @@ def pack_weights_ternary(W: torch.Tensor, *, gamma: torch.Tensor | None = None, 
                                           _ptr(Sp), _ptr(Zp), _ld(Sp), _ptr(nnz), _stream(W.device)),
            "bnn_pack_weights_ternary")
     return Sp, Zp, nnz
+
+
+# ---- the decoder's key/value cache
+
+BF16, F16, F32 = 1, 2, 3
+_KV_TYPES = {torch.bfloat16: BF16, torch.float16: F16}
+ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
+
+
+class KVCache:
+    """A paged key/value cache over the caller's tensors (bnn_kv_cache).
+
+    ``k``, ``v``: [pages, page_size, kv_heads, dim] in bfloat16 or float16,
+    any strides with a unit last one (a head-major cache is passed
+    transposed).  ``table``: int32 [B, pages per sequence], or None where
+    sequence b owns page b.  ``pos`` int32 and ``score`` float32
+    [B, kv_heads, slots]: the position and the running attention weight of
+    each slot, for the calls that keep or read them.  The tensors are kept
+    alive by this object and used in place."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor | None = None, *,
+                 pos: torch.Tensor | None = None, score: torch.Tensor | None = None):
+        if k.dtype not in _KV_TYPES:
+            raise TypeError(f"k must be torch.bfloat16 or torch.float16 (got {k.dtype})")
+        _dev(k, k.dtype, "k")
+        _dev(v, k.dtype, "v")
+        if k.dim() != 4 or k.shape != v.shape or k.stride(3) != 1 or v.stride(3) != 1:
+            raise ValueError("k and v must be [pages, page_size, kv_heads, dim] alike, with a unit last stride")
+        pages, page, heads, dim = k.shape
+        self.k, self.v, self.table, self.pos, self.score = k, v, table, pos, score
+        self.device, self.dtype = k.device, k.dtype
+        self.kv_heads, self.dim, self.page_size = heads, dim, page
+        c = self._c = _KvCache()
+        c.K, c.k_page, c.k_slot, c.k_head = k.data_ptr(), k.stride(0), k.stride(1), k.stride(2)
+        c.V, c.v_page, c.v_slot, c.v_head = v.data_ptr(), v.stride(0), v.stride(1), v.stride(2)
+        if table is not None:
+            _dev(table, torch.int32, "table")
+            if table.dim() != 2 or not table.is_contiguous():
+                raise ValueError("table must be a contiguous [B, pages per sequence] tensor")
+            c.table, c.ld_table = table.data_ptr(), table.shape[1]
+        c.num_pages, c.page_size, c.kv_heads, c.dim, c.dtype = pages, page, heads, dim, _KV_TYPES[k.dtype]
+        self.sequences = pages if table is None else table.shape[0]
+        self.slots = page if table is None else table.shape[1] * page
+        for t, dtype, name in ((pos, torch.int32, "pos"), (score, torch.float32, "score")):
+            if t is not None:
+                self._check_slots(_dev(t, dtype, name), name)
+        self._ref = ctypes.addressof(c)
+
+    def _check_slots(self, t, name):
+        if t.dim() != 3 or t.shape[1] != self.kv_heads or t.shape[2] < self.slots or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [B, kv_heads, slots] tensor of at least {self.slots} slots")
+        return t
+
+
+def _batch(cache: KVCache, indptr, ctx, rows: int, max_nodes: int, max_ctx: int) -> _KvBatch:
+    b = _KvBatch()
+    _dev(indptr, torch.int32, "indptr")
+    _dev(ctx, torch.int32, "ctx")
+    n = ctx.numel()
+    if indptr.numel() != n + 1 or n > cache.sequences or not indptr.is_contiguous() or not ctx.is_contiguous():
+        raise ValueError("indptr must be [B + 1] and ctx [B], contiguous, for at most the cache's sequences")
+    b.indptr, b.ctx, b.B, b.rows = indptr.data_ptr(), ctx.data_ptr(), n, rows
+    b.max_nodes, b.max_ctx = max_nodes, max_ctx
+    return b
+
+
+def _token_rows(t: torch.Tensor, dtype, name: str, rows, heads, dim) -> torch.Tensor:
+    _dev(t, dtype, name)
+    if t.dim() != 3 or t.stride(2) != 1 or t.shape[0] != rows or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [{rows}, {heads}, {dim}] with a unit last stride (got {tuple(t.shape)})")
+    return t
+
+
+def _bit_rows(t: torch.Tensor | None, name: str, rows: int):
+    if t is None:
+        return None, 0
+    _dev(t, torch.int32, name)
+    if t.dim() != 2 or t.shape[0] != rows or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous packed int32 [{rows}, words] tensor")
+    return t.data_ptr(), t.shape[1]
+
+
+def rope_turns(max_pos: int, rot: int, *, base: float = 10000.0, kind: str = "plain", factor: float = 1.0,
+               old_ctx: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None) -> torch.Tensor:
+    """The table of qk_norm_rope, float32 [max_pos, rot]: rot/2 cosines, then
+    rot/2 sines, computed in double (bnn_rope_turns_host).  ``kind``: "plain",
+    "linear", "base", "ramp" or "bands", the ways to stretch positions to
+    longer contexts that the header lists."""
+    t = torch.empty((int(max_pos), int(rot)), dtype=torch.float32)
+    if kind not in ROPE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(ROPE_KINDS)}")
+    _check(lib().bnn_rope_turns_host(max_pos, rot, base, ROPE_KINDS[kind], factor, old_ctx, beta_fast, beta_slow, _ptr(t)),
+           "bnn_rope_turns_host")
+    return t if device is None else t.to(device)
+
+
+def tree_mask(parents, words: int | None = None) -> torch.Tensor:
+    """Packed visibility rows of one tree of drafts, int32 [T, words] on the
+    host: bit j of row i where node j is i or an ancestor of i.
+    ``parents[i]`` < i, or -1 for a child of the last committed token."""
+    p = torch.as_tensor(parents, dtype=torch.int32).contiguous()
+    T = p.numel()
+    words = max(1, (T + 31) // 32) if words is None else int(words)
+    m = torch.zeros((T, words), dtype=torch.int32)
+    if T:
+        _check(lib().bnn_tree_mask_host(_ptr(p), T, _ptr(m), words), "bnn_tree_mask_host")
+    return m
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCache, indptr: torch.Tensor,
+                 ctx: torch.Tensor, positions: torch.Tensor, turns: torch.Tensor | None, *,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out: torch.Tensor | None = None) -> torch.Tensor:
+    """Norm and rotate the new tokens' queries and keys, append keys and
+    values to the cache at the slots after each sequence's ``ctx``
+    (bnn_qk_norm_rope).
+
+    ``q`` [rows, heads, dim], ``k``, ``v`` [rows, kv_heads, dim]: float32 or
+    the cache's type, views of one fused projection if wanted.  ``indptr``
+    int32 [B + 1], ``ctx`` int32 [B], ``positions`` int32 [rows].  ``turns``:
+    rope_turns, or None for no rotation.  Also fills the slots' ``cache.pos``
+    and clears their ``cache.score`` where the cache has them.  Returns the
+    queries in the cache's type, [rows, heads, dim]."""
+    rows, heads, dim = q.shape
+    src = q.dtype
+    if src is not torch.float32 and src is not cache.dtype:
+        raise TypeError(f"q must be torch.float32 or {cache.dtype} (got {src})")
+    _token_rows(q, src, "q", rows, heads, cache.dim)
+    _token_rows(k, src, "k", rows, cache.kv_heads, cache.dim)
+    _token_rows(v, src, "v", rows, cache.kv_heads, cache.dim)
+    _dev(positions, torch.int32, "positions")
+    if positions.numel() != rows or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous [rows] tensor")
+    b = _batch(cache, indptr, ctx, rows, rows, 0)
+    if q_out is None:
+        q_out = torch.empty((rows, heads, dim), dtype=cache.dtype, device=q.device)
+    else:
+        _token_rows(q_out, cache.dtype, "q_out", rows, heads, dim)
+    a = _RopeArgs()
+    a.q, a.q_row, a.q_head = q.data_ptr(), q.stride(0), q.stride(1)
+    a.k, a.k_row, a.k_head = k.data_ptr(), k.stride(0), k.stride(1)
+    a.v, a.v_row, a.v_head = v.data_ptr(), v.stride(0), v.stride(1)
+    a.src_dtype = F32 if src is torch.float32 else _KV_TYPES[src]
+    a.heads = heads
+    a.q_out, a.qo_row, a.qo_head = q_out.data_ptr(), q_out.stride(0), q_out.stride(1)
+    a.positions = positions.data_ptr()
+    if turns is not None:
+        _dev(turns, torch.float32, "turns")
+        if turns.dim() != 2 or not turns.is_contiguous():
+            raise ValueError("turns must be a contiguous [max_pos, rot] tensor")
+        a.turns, a.max_pos, a.rot = turns.data_ptr(), turns.shape[0], turns.shape[1]
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _dev(w, torch.float32, name)
+            if w.numel() != dim or not w.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous [{dim}] tensor")
+            setattr(a, name, w.data_ptr())
+    a.interleaved, a.eps = int(bool(interleaved)), eps
+    if cache.pos is not None:
+        a.pos, a.ld_slots = cache.pos.data_ptr(), cache.pos.shape[2]
+    if cache.score is not None:
+        if cache.pos is not None and cache.pos.shape[2] != cache.score.shape[2]:
+            raise ValueError("cache.pos and cache.score must have the same number of slots")
+        a.score, a.ld_slots = cache.score.data_ptr(), cache.score.shape[2]
+    _check(lib().bnn_qk_norm_rope(cache._ref, ctypes.addressof(b), ctypes.addressof(a), _stream(q.device)),
+           "bnn_qk_norm_rope")
+    return q_out
+
+
+def tree_attention_workspace(cache: KVCache, rows: int, heads: int, max_nodes: int, max_ctx: int) -> torch.Tensor:
+    """A workspace for tree_attention calls of up to these sizes over this
+    cache's sequences."""
+    b = _KvBatch()
+    b.B, b.rows, b.max_nodes, b.max_ctx = cache.sequences, rows, max_nodes, max_ctx
+    n = lib().bnn_tree_attention_workspace(cache._ref, ctypes.addressof(b), heads)
+    if n < 0:
+        raise ValueError("tree_attention_workspace: sizes out of range")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def tree_attention(q: torch.Tensor, cache: KVCache, indptr: torch.Tensor, ctx: torch.Tensor, *, max_nodes: int,
+                   max_ctx: int, mask: torch.Tensor | None = None, scale: float | None = None,
+                   out: torch.Tensor | None = None, lse: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                   workspace: torch.Tensor | None = None):
+    """Attention of the new tokens' queries over the cache (bnn_tree_attention).
+
+    ``q`` [rows, heads, dim] in the cache's type; ``mask``: packed int32
+    [rows, words] (tree_mask), None for a causal run.  ``max_nodes`` and
+    ``max_ctx`` bound the new and committed tokens of a sequence.  Returns
+    (out [rows, heads, dim] in ``out_dtype``: float32, or the cache's type by
+    default; lse float32 [rows, heads], the logarithm of each row's sum)."""
+    rows, heads, dim = q.shape
+    _token_rows(q, cache.dtype, "q", rows, heads, cache.dim)
+    b = _batch(cache, indptr, ctx, rows, max_nodes, max_ctx)
+    if out is None:
+        out = torch.empty((rows, heads, dim), dtype=out_dtype or cache.dtype, device=q.device)
+    else:
+        _token_rows(out, out.dtype, "out", rows, heads, dim)
+    if out.dtype is not torch.float32 and out.dtype is not cache.dtype:
+        raise TypeError(f"out must be torch.float32 or {cache.dtype} (got {out.dtype})")
+    if lse is None:
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
+    _dev(lse, torch.float32, "lse")
+    if lse.shape != (rows, heads):
+        raise ValueError(f"lse must be [{rows}, {heads}]")
+    if workspace is None:
+        workspace = torch.empty(max(0, lib().bnn_tree_attention_workspace(cache._ref, ctypes.addressof(b), heads)),
+                                dtype=torch.uint8, device=q.device)
+    a = _AttnArgs()
+    a.q, a.q_row, a.q_head, a.heads = q.data_ptr(), q.stride(0), q.stride(1), heads
+    a.mask, a.ld_mask = _bit_rows(mask, "mask", rows)
+    a.scale = dim ** -0.5 if scale is None else scale
+    a.out, a.o_row, a.o_head = out.data_ptr(), out.stride(0), out.stride(1)
+    a.out_dtype = F32 if out.dtype is torch.float32 else _KV_TYPES[out.dtype]
+    a.lse, a.ld_lse = lse.data_ptr(), _ld(lse)
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib().bnn_tree_attention(cache._ref, ctypes.addressof(b), ctypes.addressof(a), _stream(q.device)),
+           "bnn_tree_attention")
+    return out, lse
+
+
+def cache_score_add(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, indptr: torch.Tensor, ctx: torch.Tensor, *,
+                    max_nodes: int, max_ctx: int, mask: torch.Tensor | None = None, accept: torch.Tensor | None = None,
+                    scale: float | None = None, score_out: torch.Tensor | None = None) -> torch.Tensor:
+    """Add to ``cache.score`` the attention weight that each slot received
+    from the accepted new tokens (bnn_cache_score_add).  ``q``, ``mask``,
+    ``scale``: as given to tree_attention; ``lse``: as it returned it;
+    ``accept``: packed int32 [B, words], None where all tokens count.  Writes
+    the sums in place, or into ``score_out``, and returns them."""
+    rows, heads, dim = q.shape
+    _token_rows(q, cache.dtype, "q", rows, heads, cache.dim)
+    if cache.score is None:
+        raise ValueError("the cache has no score tensor")
+    b = _batch(cache, indptr, ctx, rows, max_nodes, max_ctx)
+    _dev(lse, torch.float32, "lse")
+    if lse.shape != (rows, heads):
+        raise ValueError(f"lse must be [{rows}, {heads}]")
+    if score_out is None:
+        score_out = cache.score
+    elif _dev(score_out, torch.float32, "score_out").shape != cache.score.shape or not score_out.is_contiguous():
+        raise ValueError("score_out must be laid out as cache.score")
+    a = _ScoreArgs()
+    a.q, a.q_row, a.q_head, a.heads = q.data_ptr(), q.stride(0), q.stride(1), heads
+    a.lse, a.ld_lse = lse.data_ptr(), _ld(lse)
+    a.mask, a.ld_mask = _bit_rows(mask, "mask", rows)
+    a.accept, a.ld_accept = _bit_rows(accept, "accept", b.B)
+    a.scale = dim ** -0.5 if scale is None else scale
+    a.score_in, a.score_out, a.ld_slots = cache.score.data_ptr(), score_out.data_ptr(), cache.score.shape[2]
+    _check(lib().bnn_cache_score_add(cache._ref, ctypes.addressof(b), ctypes.addressof(a), _stream(q.device)),
+           "bnn_cache_score_add")
+    return score_out
+
+
+def cache_evict_workspace(cache: KVCache) -> torch.Tensor:
+    """A workspace for cache_evict calls on this cache."""
+    n = lib().bnn_cache_evict_workspace(cache._ref, cache.sequences)
+    if n < 0:
+        raise ValueError("cache_evict_workspace: sizes out of range")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def cache_evict(cache: KVCache, indptr: torch.Tensor, ctx: torch.Tensor, *, budget: int, recent: int, max_nodes: int,
+                max_ctx: int, accept: torch.Tensor | None = None, ctx_out: torch.Tensor | None = None,
+                pos_out: torch.Tensor | None = None, score_out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Drop the new tokens that were not accepted and cut every sequence to
+    ``budget`` tokens per key head by ``cache.score``, keeping the last
+    ``recent`` positions first (bnn_cache_evict).  K and V are compacted in
+    place; ``cache.pos``, ``cache.score`` and ``ctx`` too unless outputs are
+    given.  Returns the new ctx, int32 [B]."""
+    if cache.pos is None or cache.score is None:
+        raise ValueError("the cache has no pos or no score tensor")
+    if cache.pos.shape != cache.score.shape:
+        raise ValueError("cache.pos and cache.score must have the same shape")
+    b = _batch(cache, indptr, ctx, 1 << 30, max_nodes, max_ctx)
+    pos_out = cache.pos if pos_out is None else _dev(pos_out, torch.int32, "pos_out")
+    score_out = cache.score if score_out is None else _dev(score_out, torch.float32, "score_out")
+    ctx_out = ctx if ctx_out is None else _dev(ctx_out, torch.int32, "ctx_out")
+    for t in (pos_out, score_out):
+        if t.shape != cache.pos.shape or not t.is_contiguous():
+            raise ValueError("pos_out and score_out must be laid out as cache.pos")
+    if ctx_out.shape != ctx.shape or not ctx_out.is_contiguous():
+        raise ValueError("ctx_out must be laid out as ctx")
+    if workspace is None:
+        workspace = cache_evict_workspace(cache)
+    a = _EvictArgs()
+    a.accept, a.ld_accept = _bit_rows(accept, "accept", b.B)
+    a.budget, a.recent = budget, recent
+    a.pos_in, a.pos_out = cache.pos.data_ptr(), pos_out.data_ptr()
+    a.score_in, a.score_out = cache.score.data_ptr(), score_out.data_ptr()
+    a.ld_slots = cache.pos.shape[2]
+    a.ctx_out = ctx_out.data_ptr()
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib().bnn_cache_evict(cache._ref, ctypes.addressof(b), ctypes.addressof(a), _stream(cache.device)),
+           "bnn_cache_evict")
+    return ctx_out
