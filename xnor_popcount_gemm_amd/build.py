@@ -70,7 +70,9 @@ def build_calib(verbose: bool = False) -> str:
 # layer's loop-carried accumulators in VGPRs but let the MFMAs write AGPRs,
 # and copied all 64 accumulator registers across and back every K chunk
 # (4 VALU ops per MFMA in a loop of 32 MFMAs).
-FILE_FLAGS = {"dense.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# The attention kernels keep their accumulators in VGPRs for the same reason.
+_VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+FILE_FLAGS = {name: _VGPR_FORM for name in ("dense.hip", "attn_bf16.hip", "attn_bf16_f32.hip", "attn_f16.hip", "attn_f16_f32.hip")}
 
 
 def build(verbose: bool = False) -> str:

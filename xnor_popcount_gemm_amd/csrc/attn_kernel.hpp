@@ -1,0 +1,626 @@
+// Attention of a step's new tokens over the paged cache, on the matrix cores.
+//
+//     s_j = scale <q, k_j> ;  out = sum_j exp(s_j - lse) v_j ;  lse = ln sum_j exp(s_j)
+//
+// The rows of a (sequence, key head) are its new tokens times the query heads
+// that share the key head, so one pass over K and V serves them all.
+//
+// Products.  Scores are computed transposed, S^T = K Q^T: a lane then holds
+// one row's scores for 8 or 16 of a step's 32 slots, so the softmax
+// statistics are a few in-lane operations and one or two lane swaps, and the
+// weights are already laid out as the second operand of O^T = V^T P^T: no
+// weight crosses a lane.  What V^T needs is a transposed read of V's rows,
+// which ds_read_b64_tr_b16 gives.  R = 16 rows per wave use 16x16x32 matrix
+// instructions, R = 32 rows 32x32x16.
+//
+// Running maximum.  Weights are taken relative to a reference that is only
+// raised when a score passes it by more than 2^8 (in the base-2 logarithm):
+// the result is the same, and the accumulators are rescaled a few times
+// instead of at every step.
+//
+// Tiles.  K and V rows go from global memory straight to LDS (16 bytes per
+// lane), two buffers deep: the next step's rows are in flight while one is
+// worked on.  16 slots of 32 dimensions form a 1 KiB block, slot r at 64 r
+// bytes, its four 16-byte pieces permuted by XOR so that the 8 lanes served
+// together read different banks: by (r >> 1) & 3 for K (b128 reads of one
+// piece of 8 slots), by 2 ((r >> 1) & 1) for V (transposed reads of two
+// pieces of 4 slots).  Rows past the end are read from a block of zeros.
+//
+// Masks.  Committed slots are seen by every row and cost nothing; the steps
+// that hold new tokens run in a loop of their own and take one 32-bit word per
+// row and 32 slots.  An unseen token must not matter even where its V is NaN
+// or infinite, and 0 * NaN is NaN, so that loop takes such values as 0 in the
+// products and notes, as bits per row and dimension, which rows saw an
+// infinity of which sign (NaN: both); the infinities are added at the end.
+#pragma once
+
+#include <math.h>
+
+#include <type_traits>
+
+#include "bnn_device.hpp"
+#include "kv_launch.hpp"
+
+namespace bnn {
+
+// How a call is cut into workgroups, from what the host knows.
+struct AttnPlan {
+    int32_t R, RW, KW;     // rows per wave, waves along rows, waves along slots
+    int32_t row_tiles;     // of a (sequence, key head), at most
+    int32_t chunk;         // slots per workgroup
+    int32_t chunks;        // of a sequence, at most
+};
+
+namespace {
+
+__device__ __align__(64) const uint32_t zero_row[128] = {};
+
+template <typename T> struct Mma;
+template <> struct Mma<Bf16> {
+    static __device__ __forceinline__ f32x16 m32(bf16x8 a, bf16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ f32x4 m16(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+};
+template <> struct Mma<F16> {
+    static __device__ __forceinline__ f32x16 m32(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ f32x4 m16(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+};
+
+// 16 bytes per lane from g to LDS at lds + 16 * lane.  In asm so that the
+// compiler does not make every LDS read wait for it; the caller waits.
+__device__ __forceinline__ void dma16(const char* g, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(g) : "memory");
+}
+
+__device__ __forceinline__ void wait_all() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+
+// Maximum / sum over the lanes that hold one row: l ^ 32, and l ^ 16 for 16 rows.
+template <int R>
+__device__ __forceinline__ float row_max(float x) {
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    if (R == 16) {
+        auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+    }
+    return x;
+}
+
+template <int R>
+__device__ __forceinline__ float row_sum(float x) {
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    if (R == 16) {
+        auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(q[0]) + __uint_as_float(q[1]);
+    }
+    return x;
+}
+
+template <int R> struct Acc;
+template <> struct Acc<16> { typedef f32x4 type; };
+template <> struct Acc<32> { typedef f32x16 type; };
+
+// Partial results of a chunk: out rows and (maximum, sum) per row.
+__host__ __device__ inline int64_t part_rows(int64_t rows, int64_t heads) { return rows * heads; }
+
+template <typename T, int D, int R, int RW, int KW, int NS, typename O>
+struct Attn {
+    typedef typename T::vec8 vec8;
+    typedef typename T::vec4 vec4;
+    typedef typename T::elem elem;
+    typedef typename Acc<R>::type acc;
+
+    static constexpr int WAVES = RW * KW;
+    static constexpr int BN = RW == 4 && D < 256 ? 64 : 32;     // slots per step and slot group
+    static constexpr int SUB = BN / 32;
+    static constexpr int NSC = R / 2;                           // scores per lane and 32 slots
+    static constexpr int QS = R == 32 ? D / 16 : D / 32;        // products of a 32-slot score block
+    static constexpr int OB = R == 32 ? D / 32 : D / 16;        // accumulator blocks
+    static constexpr int GRP = 32 * D;                          // bytes of 16 slots
+    static constexpr int VOFF = BN * D * 2;                     // V after K in a buffer
+    static constexpr int STAGE = 2 * VOFF;
+    static constexpr int GROUP_LDS = 2 * STAGE;                 // two buffers of a slot group
+    static constexpr int OPAD = D + 4;
+    static constexpr int MERGE = KW > 1 ? KW * RW * R * OPAD * 4 + KW * RW * R * 8 : 4 * 32 * 36 * 4;
+    static constexpr int LDS = KW * GROUP_LDS > MERGE ? KW * GROUP_LDS : MERGE;
+    // 16-slot groups that a wave fetches per step, and whether it fetches both K and V of them
+    static constexpr int FETCH = RW == 1 ? 2 : 1;
+    static constexpr bool SPLIT_KV = RW == 4 && BN == 32;
+
+    static __device__ __forceinline__ int slot_of(int i, int lane) {
+        return R == 32 ? 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) : 16 * (i >> 2) + 4 * (lane >> 4) + (i & 3);
+    }
+
+    static __device__ __forceinline__ vec8 v_frag(const char* base, int o) {
+        typedef __attribute__((address_space(3))) s16x4* tp;
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tp)(base + o));
+        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tp)(base + o + (R == 32 ? 512 : GRP)));
+        return __builtin_bit_cast(vec8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+
+    static constexpr int PW = (OB * (int)sizeof(acc) / 4 + 31) / 32;   // words of a bit per accumulator
+
+    // Whether the low 16 bits are NaN or an infinity.
+    static __device__ __forceinline__ uint32_t special(uint32_t h) { return (h & T::special) == T::special; }
+
+    // NaN and infinities as 0.
+    static __device__ __forceinline__ vec8 finite(vec8 v) {
+        u32x4 x = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (special(x[i])) x[i] &= 0xFFFF0000u;
+            if (special(x[i] >> 16)) x[i] &= 0x0000FFFFu;
+        }
+        return __builtin_bit_cast(vec8, x);
+    }
+
+    static __device__ __forceinline__ acc mma(vec8 a, vec8 b, acc c) {
+        if constexpr (R == 32) return Mma<T>::m32(a, b, c);
+        else return Mma<T>::m16(a, b, c);
+    }
+};
+
+template <typename T, int D, int R, int RW, int KW, int NS, typename O>
+__global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_attention(KvCache c, KvBatch b, AttnArgs a, AttnPlan pl) {
+    typedef Attn<T, D, R, RW, KW, NS, O> A;
+    typedef typename A::vec8 vec8;
+    typedef typename A::acc acc;
+    __shared__ __align__(1024) char lds[A::LDS];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int rw = wave % RW, kw = wave / RW;
+    const int rt = blockIdx.x / pl.chunks, ci = blockIdx.x % pl.chunks, kh = blockIdx.y, seq = blockIdx.z;
+
+    const Seq sq = sequence(c, b, seq);
+    const int nodes = sq.nodes < b.max_nodes ? sq.nodes : b.max_nodes;
+    const int rows = nodes * a.group, tile0 = rt * R * RW;
+    if (tile0 >= rows) return;
+    int nchunk = (sq.total + pl.chunk - 1) / pl.chunk;
+    nchunk = nchunk < 1 ? 1 : nchunk > pl.chunks ? pl.chunks : nchunk;
+    if (ci >= nchunk) return;
+    // slots of this workgroup; without a mask none past the last row's own
+    const int last_row = (tile0 + R * RW < rows ? tile0 + R * RW : rows) - 1;
+    int end = sq.total;
+    if (!a.mask) { const int64_t own = (int64_t)sq.ctx + last_row / a.group + 1; end = own < end ? (int)own : end; }
+    const int k0 = ci * pl.chunk;
+    int k1 = ci == nchunk - 1 ? end : k0 + pl.chunk;
+    k1 = k1 < end ? k1 : end;
+    const int steps = k1 > k0 ? (k1 - k0 + KW * A::BN - 1) / (KW * A::BN) : 0;
+
+    // this lane's row and its query, the second operand of S^T = K Q^T
+    const int lr = lane & (R - 1);
+    const int r = tile0 + rw * R + lr;
+    const bool live = r < rows;
+    const int node = live ? r / a.group : 0;
+    const int64_t row = sq.row0 + node;
+    const int head = kh * a.group + (live ? r - node * a.group : 0);
+    const float c2 = fabsf(a.scale) * 1.44269504088896340736f;
+    vec8 qf[A::QS];
+    {
+        const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+        const char* q = a.q + row * a.q_row + head * a.q_head + (lane / R) * 16;
+#pragma unroll
+        for (int s = 0; s < A::QS; ++s) {
+            u32x4 x = {0, 0, 0, 0};
+            if (live) x = *(const u32x4*)(q + s * (R == 32 ? 32 : 64));
+            x ^= flip;
+            qf[s] = __builtin_bit_cast(vec8, x);
+        }
+    }
+
+    // fetch of K and V rows: a lane takes 16-byte pieces of slot lane / 4 of a 16-slot group
+    char* const my = lds + kw * A::GROUP_LDS;
+    const uint32_t my_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)my;
+    const int fr = lane >> 2;
+    const int kpiece = ((lane & 3) ^ ((fr >> 1) & 3)) * 16, vpiece = ((lane & 3) ^ (2 * ((fr >> 1) & 1))) * 16;
+    const char* const kbase = c.K + kh * c.k_head + kpiece;
+    const char* const vbase = c.V + kh * c.v_head + vpiece;
+    const int32_t* const table = c.table ? c.table + (int64_t)seq * c.ld_table : nullptr;
+    int32_t entry[A::FETCH];
+    uint32_t place[A::FETCH];
+    auto lookup = [&](int step) {
+#pragma unroll
+        for (int f = 0; f < A::FETCH; ++f) {
+            const int g = RW == 1 ? f : rw % (A::BN / 16);
+            const int slot = k0 + (step * KW + kw) * A::BN + 16 * g + fr;
+            entry[f] = -1;
+            if (slot < k1) {
+                const uint32_t p = fastdiv(slot, c.page);
+                place[f] = slot - p * c.page.d;
+                entry[f] = table ? table[p] : seq;
+            }
+        }
+    };
+    auto fetch = [&](int buf) {
+#pragma unroll
+        for (int f = 0; f < A::FETCH; ++f) {
+            const int g = RW == 1 ? f : rw % (A::BN / 16);
+            const bool there = (uint32_t)entry[f] < c.num_pages;
+            const uint32_t to = my_lds + buf * A::STAGE + g * A::GRP;
+            if (!A::SPLIT_KV || rw < 2) {
+                const char* p = there ? kbase + entry[f] * c.k_page + place[f] * c.k_slot : (const char*)zero_row;
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) dma16(p + 64 * j, to + 1024 * j);
+            }
+            if (!A::SPLIT_KV || rw >= 2) {
+                const char* p = there ? vbase + entry[f] * c.v_page + place[f] * c.v_slot : (const char*)zero_row;
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) dma16(p + 64 * j, to + A::VOFF + 1024 * j);
+            }
+        }
+    };
+
+    // LDS offsets of this lane's operand reads
+    int kread[2], vread[2];
+    if constexpr (R == 32) {
+        const int s = lane & 15, hi = lane >> 5, z = (s >> 1) & 3;
+        const int base = ((lane >> 4) & 1) * A::GRP + s * 64;
+        kread[0] = base + ((hi ^ z) * 16);
+        kread[1] = base + (((2 + hi) ^ z) * 16);
+        const int i = lane & 15, d = (lane >> 4) & 1, key = 4 * hi + (i >> 2);
+        vread[0] = A::VOFF + key * 64 + (((2 * d + ((i & 3) >> 1)) ^ (2 * ((key >> 1) & 1))) * 16) + (i & 1) * 8;
+        vread[1] = vread[0];
+    } else {
+        const int s = lane & 15, quad = lane >> 4, z = (s >> 1) & 3;
+        kread[0] = kread[1] = s * 64 + ((quad ^ z) * 16);
+        const int key = 4 * quad + (s >> 2), zv = 2 * ((key >> 1) & 1);
+        vread[0] = A::VOFF + key * 64 + ((((s & 3) >> 1) ^ zv) * 16) + (s & 1) * 8;
+        vread[1] = A::VOFF + key * 64 + (((2 + ((s & 3) >> 1)) ^ zv) * 16) + (s & 1) * 8;
+    }
+
+    acc o[A::OB];
+#pragma unroll
+    for (int i = 0; i < A::OB; ++i) o[i] = acc{};
+    float m = -INFINITY, l = 0.f;   // reference (base-2 logarithm) and this lane's share of the sum
+    // which of this lane's dimensions saw +inf / -inf: bit 4 i + e of dimension e of its piece i of 4
+    uint32_t plus[A::PW], minus[A::PW];
+#pragma unroll
+    for (int i = 0; i < A::PW; ++i) plus[i] = minus[i] = 0;
+
+    // one step: BN slots from kb0 on, in the buffer buf
+    auto work = [&](auto is_masked, const char* buf, const int kb0) {
+        constexpr bool MASKED = decltype(is_masked)::value;
+#pragma unroll
+        for (int sub = 0; sub < A::SUB; ++sub) {
+            const int kb = kb0 + 32 * sub;
+            uint32_t vis = 0xFFFFFFFFu;
+            if (MASKED) {
+                if (kb >= k1) break;
+                const int rel = kb - sq.ctx;
+                if (live && rel > -32) {
+                    if (!a.mask) {
+                        const int n = node - rel + 1;
+                        vis = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+                    } else {
+                        const uint32_t* mr = a.mask + row * a.ld_mask;
+                        if (rel >= 0) {
+                            const int w = rel >> 5;
+                            const uint64_t lo = w < a.ld_mask ? mr[w] : 0u, hi = w + 1 < a.ld_mask ? mr[w + 1] : 0u;
+                            vis = (uint32_t)((lo | hi << 32) >> (rel & 31));
+                        } else {
+                            vis = (mr[0] << -rel) | ((1u << -rel) - 1);
+                        }
+                    }
+                }
+                if (k1 - kb < 32) vis &= (1u << (k1 - kb)) - 1;
+                if (!__any(live && vis != 0)) continue;
+            }
+
+            // scores
+            float sc[A::NSC];
+            if constexpr (R == 32) {
+                f32x16 s = {};
+#pragma unroll
+                for (int q = 0; q < A::QS; ++q)
+                    s = Mma<T>::m32(*(const vec8*)(buf + sub * 2 * A::GRP + kread[q & 1] + (q >> 1) * 1024), qf[q], s);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sc[i] = s[i];
+            } else {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    f32x4 s = {};
+#pragma unroll
+                    for (int q = 0; q < A::QS; ++q)
+                        s = Mma<T>::m16(*(const vec8*)(buf + g * A::GRP + kread[0] + q * 1024), qf[q], s);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[4 * g + i] = s[i];
+                }
+            }
+            if (MASKED) {
+#pragma unroll
+                for (int i = 0; i < A::NSC; ++i) sc[i] = (vis >> A::slot_of(i, lane)) & 1u ? sc[i] : -INFINITY;
+            }
+            float mx = sc[0];
+#pragma unroll
+            for (int i = 1; i < A::NSC; ++i) mx = fmaxf(mx, sc[i]);
+            mx = row_max<R>(mx) * c2;
+            if (__any(mx > m + 8.f)) {
+                const float mn = fmaxf(m, mx);
+                const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < A::OB; ++i) o[i] *= f;
+            }
+            const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int i = 0; i < A::NSC; ++i) sc[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], c2, -ms));
+            if (MASKED) {   // a scale of 0 makes NaN of the unseen ones' -inf
+#pragma unroll
+                for (int i = 0; i < A::NSC; ++i) sc[i] = (vis >> A::slot_of(i, lane)) & 1u ? sc[i] : 0.f;
+            }
+            float ls = 0.f;
+#pragma unroll
+            for (int i = 0; i < A::NSC; ++i) ls += sc[i];
+            l += ls;
+
+            // weights as 16-bit operands: one term, or as many as keep them whole
+            vec8 pf[A::NSC / 8][NS];
+#pragma unroll
+            for (int g = 0; g < A::NSC / 8; ++g) {
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const typename A::elem p = (typename A::elem)sc[8 * g + i];
+                        pf[g][n][i] = p;
+                        if (n + 1 < NS) sc[8 * g + i] -= (float)p;
+                    }
+            }
+            const char* vb = buf + sub * 2 * A::GRP;
+#pragma unroll
+            for (int g = 0; g < A::NSC / 8; ++g)
+#pragma unroll
+                for (int i = 0; i < A::OB; ++i) {
+                    vec8 v = R == 32 ? A::v_frag(vb, vread[0] + g * A::GRP + i * 1024)
+                                     : A::v_frag(vb, vread[i & 1] + (i >> 1) * 1024);
+                    if (MASKED) v = A::finite(v);
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) o[i] = A::mma(v, pf[g][n], o[i]);
+                }
+            if (MASKED) {
+                uint32_t bad = 0;
+#pragma unroll 4
+                for (int i = 0; i < D / 16; ++i) {
+                    const u32x4 x = *(const u32x4*)(vb + A::VOFF + (i * 64 + lane) * 16);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) bad |= A::special(x[j]) | A::special(x[j] >> 16);
+                }
+                if (__any(bad)) {   // rare: slot by slot
+#pragma unroll 1
+                    for (int key = 0; key < 32; ++key) {
+                        const bool saw = (vis >> key) & 1u;
+                        const char* vr = vb + A::VOFF + (key >> 4) * A::GRP + (key & 15) * 64;
+                        const int z = 2 * ((key >> 1) & 1);
+#pragma unroll
+                        for (int w = 0; w < A::PW; ++w) {
+                            uint32_t up = 0, down = 0;
+#pragma unroll 1
+                            for (int q = 0; q < 8; ++q) {
+                                const int piece = 8 * w + q;   // 4 dimensions of this lane's row
+                                if (piece >= A::OB * (R == 32 ? 4 : 1)) break;
+                                const int d = R == 32 ? 8 * piece + 4 * (lane >> 5) : 16 * piece + 4 * (lane >> 4);
+                                const u32x2 x = *(const u32x2*)(vr + (d >> 5) * 1024 + ((((d >> 3) & 3) ^ z) * 16) + (d & 4) * 2);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t h = (e < 2 ? x[0] : x[1]) >> (16 * (e & 1)) & 0xFFFFu;
+                                    const bool nan = (h & 0x7FFFu) > T::special;
+                                    up |= (uint32_t)(nan || h == T::special) << (4 * q + e);
+                                    down |= (uint32_t)(nan || h == (T::special | 0x8000u)) << (4 * q + e);
+                                }
+                            }
+                            plus[w] |= saw ? up : 0u;
+                            minus[w] |= saw ? down : 0u;
+                        }
+                    }
+                }
+            }
+        }
+    };
+
+    // steps whose slots are all committed and inside the chunk, then the others
+    const int sure = k1 < sq.ctx ? k1 : sq.ctx;
+    int plain = sure > k0 ? (sure - k0) / (KW * A::BN) : 0;
+    plain = plain < steps ? plain : steps;
+    if (steps > 0) {
+        lookup(0);
+        fetch(0);
+        if (steps > 1) lookup(1);
+    }
+    auto next = [&](int st) {   // step st is in LDS; the next one is on its way
+        wait_all();
+        if (RW > 1) __builtin_amdgcn_s_barrier();
+        if (st + 1 < steps) {
+            fetch((st + 1) & 1);
+            if (st + 2 < steps) lookup(st + 2);
+        }
+        return my + (st & 1) * A::STAGE;
+    };
+    int st = 0;
+    for (; st < plain; ++st) {
+        const char* buf = next(st);
+        work(std::false_type{}, buf, k0 + (st * KW + kw) * A::BN);
+    }
+    for (; st < steps; ++st) {
+        const char* buf = next(st);
+        work(std::true_type{}, buf, k0 + (st * KW + kw) * A::BN);
+    }
+    {
+        uint32_t any = 0;
+#pragma unroll
+        for (int w = 0; w < A::PW; ++w) any |= plus[w] | minus[w];
+        if (__any(any)) {
+#pragma unroll
+            for (int i = 0; i < A::OB; ++i)
+#pragma unroll
+                for (int e = 0; e < (int)(sizeof(acc) / 4); ++e) {
+                    const int at = (int)(sizeof(acc) / 4) * i + e;
+                    if (plus[at / 32] >> (at % 32) & 1u) o[i][e] += INFINITY;
+                    if (minus[at / 32] >> (at % 32) & 1u) o[i][e] -= INFINITY;
+                }
+        }
+    }
+
+    // join the slot groups of the workgroup, then write rows
+    l = row_sum<R>(l);
+    const bool last = nchunk == 1;
+    const int64_t prow = part_rows(b.rows, a.heads);
+    float* const pout = (float*)a.work;
+    float2* const pml = (float2*)(a.work + (int64_t)pl.chunks * prow * D * 4);
+    __syncthreads();
+    if constexpr (KW > 1) {
+        float* const ol = (float*)lds;
+        float2* const ml = (float2*)(lds + KW * RW * R * A::OPAD * 4);
+        if (lane < R) ml[(kw * RW + rw) * R + lr] = make_float2(m, l);
+        __syncthreads();
+        float M = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < KW; ++k) M = fmaxf(M, ml[(k * RW + rw) * R + lr].x);
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - M);
+        float* mine = ol + ((kw * RW + rw) * R + lr) * A::OPAD;
+        if constexpr (R == 32) {
+#pragma unroll
+            for (int i = 0; i < A::OB; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *(f32x4*)(mine + 32 * i + 8 * q + 4 * (lane >> 5)) = f32x4{o[i][4 * q], o[i][4 * q + 1], o[i][4 * q + 2], o[i][4 * q + 3]} * f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < A::OB; ++i) *(f32x4*)(mine + 16 * i + 4 * (lane >> 4)) = *(const f32x4*)&o[i] * f;
+        }
+        __syncthreads();
+        constexpr int PER = D / 4, N = RW * R * PER;
+        for (int e = tid; e < N; e += RW * KW * 64) {
+            const int tr = e / PER, d = (e % PER) * 4, rr = tile0 + tr;
+            if (rr >= rows) continue;
+            float Mr = -INFINITY, lr_ = 0.f;
+#pragma unroll
+            for (int k = 0; k < KW; ++k) Mr = fmaxf(Mr, ml[k * RW * R + tr].x);
+#pragma unroll
+            for (int k = 0; k < KW; ++k) {
+                const float2 x = ml[k * RW * R + tr];
+                if (x.x != -INFINITY) lr_ += x.y * __builtin_amdgcn_exp2f(x.x - Mr);
+            }
+            f32x4 y = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < KW; ++k) y += *(const f32x4*)(ol + (k * RW * R + tr) * A::OPAD + d);
+            const int nd = rr / a.group;
+            const int64_t orow = sq.row0 + nd;
+            const int oh = kh * a.group + rr - nd * a.group;
+            if (last) {
+                y *= lr_ == 0.f ? 0.f : 1.f / lr_;
+                typedef O ov __attribute__((ext_vector_type(4)));
+                *(ov*)(a.out + orow * a.o_row + oh * a.o_head + d * sizeof(O)) = __builtin_convertvector(y, ov);
+                if (d == 0 && a.lse) a.lse[orow * a.ld_lse + oh] = lr_ == 0.f ? -INFINITY : (Mr + log2f(lr_)) * 0.69314718055994530942f;
+            } else {
+                const int64_t at = ci * prow + orow * a.heads + oh;
+                *(f32x4*)(pout + at * D + d) = y;
+                if (d == 0) pml[at] = make_float2(Mr, lr_);
+            }
+        }
+    } else {
+        // 32 dimensions of the wave's rows at a time through LDS: whole row pieces leave together
+        float* const mine = (float*)lds + wave * 32 * 36;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int i = 0; i < A::OB; ++i) {
+            const acc x = last ? o[i] * inv : o[i];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *(f32x4*)(mine + lr * 36 + 8 * q + 4 * (lane >> 5)) = f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int tr = p * 8 + (lane >> 3), rr = tile0 + rw * R + tr;
+                const f32x4 y = *(const f32x4*)(mine + tr * 36 + (lane & 7) * 4);
+                if (rr < rows) {
+                    const int nd = rr / a.group, d = 32 * i + (lane & 7) * 4;
+                    const int64_t orow = sq.row0 + nd;
+                    const int oh = kh * a.group + rr - nd * a.group;
+                    if (last) {
+                        typedef O ov __attribute__((ext_vector_type(4)));
+                        *(ov*)(a.out + orow * a.o_row + oh * a.o_head + d * sizeof(O)) = __builtin_convertvector(y, ov);
+                    } else {
+                        *(f32x4*)(pout + (ci * prow + orow * a.heads + oh) * D + d) = y;
+                    }
+                }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+        if (live && lane < R) {
+            if (!last) pml[ci * prow + row * a.heads + head] = make_float2(m, l);
+            else if (a.lse) a.lse[row * a.ld_lse + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+        }
+    }
+}
+
+// Joins the chunks of the rows whose sequence was cut.  D / 4 lanes per (row, head).
+template <int D, typename O>
+__global__ __launch_bounds__(256) void k_join_chunks(KvCache c, KvBatch b, AttnArgs a, AttnPlan pl) {
+    constexpr int PER = D / 4, ROWS = 256 / PER;
+    const int row = blockIdx.x, tid = threadIdx.x;
+    const int seq = row_sequence(b, row, tid & 63);
+    if (seq < 0) return;
+    const Seq sq = sequence(c, b, seq);
+    int nchunk = (sq.total + pl.chunk - 1) / pl.chunk;
+    nchunk = nchunk > pl.chunks ? pl.chunks : nchunk;
+    if (nchunk <= 1 || row - sq.row0 >= b.max_nodes) return;
+    const int h = blockIdx.y * ROWS + tid / PER, d = (tid % PER) * 4;
+    if (tid / PER >= ROWS || h >= a.heads) return;
+    const int64_t prow = part_rows(b.rows, a.heads);
+    const float* pout = (const float*)a.work;
+    const float2* pml = (const float2*)(a.work + (int64_t)pl.chunks * prow * D * 4);
+    const int64_t at = (int64_t)row * a.heads + h;
+    float M = -INFINITY, l = 0.f;
+    for (int k = 0; k < nchunk; ++k) M = fmaxf(M, pml[k * prow + at].x);
+    f32x4 y = {0, 0, 0, 0};
+    for (int k = 0; k < nchunk; ++k) {
+        const float2 x = pml[k * prow + at];
+        if (x.x == -INFINITY) continue;
+        const float f = __builtin_amdgcn_exp2f(x.x - M);
+        l += x.y * f;
+        y += *(const f32x4*)(pout + (k * prow + at) * D + d) * f;
+    }
+    y *= l == 0.f ? 0.f : 1.f / l;
+    typedef O ov __attribute__((ext_vector_type(4)));
+    *(ov*)(a.out + row * a.o_row + h * a.o_head + d * sizeof(O)) = __builtin_convertvector(y, ov);
+    if (d == 0 && a.lse) a.lse[row * a.ld_lse + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994530942f;
+}
+
+template <typename T, int D, int R, int RW, int KW, int NS, typename O>
+void launch_tiles(const KvCache& c, const KvBatch& b, const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
+    const dim3 grid((unsigned)(pl.chunks * pl.row_tiles), c.kv_heads, b.B);
+    hipLaunchKernelGGL((k_tree_attention<T, D, R, RW, KW, NS, O>), grid, dim3(RW * KW * 64), 0, s, c, b, a, pl);
+}
+
+template <typename T, int D, int NS, typename O>
+hipError_t launch_dim(const KvCache& c, const KvBatch& b, const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
+    constexpr int KW = D == 256 ? 2 : 4;
+    if (pl.R == 16) launch_tiles<T, D, 16, 1, KW, NS, O>(c, b, a, pl, s);
+    else if (pl.RW == 1) launch_tiles<T, D, 32, 1, KW, NS, O>(c, b, a, pl, s);
+    else if (pl.RW == 2) launch_tiles<T, D, 32, 2, 2, NS, O>(c, b, a, pl, s);
+    else launch_tiles<T, D, 32, 4, 1, NS, O>(c, b, a, pl, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || pl.chunks == 1) return e;
+    constexpr int ROWS = 256 / (D / 4);
+    hipLaunchKernelGGL((k_join_chunks<D, O>), dim3(b.rows, (a.heads + ROWS - 1) / ROWS), dim3(256), 0, s, c, b, a, pl);
+    return hipGetLastError();
+}
+
+template <typename T, int NS, typename O>
+hipError_t launch_type(const KvCache& c, const KvBatch& b, const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
+    if (c.dim == 64) return launch_dim<T, 64, NS, O>(c, b, a, pl, s);
+    if (c.dim == 96) return launch_dim<T, 96, NS, O>(c, b, a, pl, s);
+    if (c.dim == 128) return launch_dim<T, 128, NS, O>(c, b, a, pl, s);
+    return launch_dim<T, 256, NS, O>(c, b, a, pl, s);
+}
+
+}  // namespace
+
+// One instantiation per file (attn_*.hip): the cache's type and the output's.
+hipError_t attn_bf16(const KvCache&, const KvBatch&, const AttnArgs&, const AttnPlan&, hipStream_t);
+hipError_t attn_bf16_f32(const KvCache&, const KvBatch&, const AttnArgs&, const AttnPlan&, hipStream_t);
+hipError_t attn_f16(const KvCache&, const KvBatch&, const AttnArgs&, const AttnPlan&, hipStream_t);
+hipError_t attn_f16_f32(const KvCache&, const KvBatch&, const AttnArgs&, const AttnPlan&, hipStream_t);
+
+}  // namespace bnn
