@@ -53,8 +53,6 @@ struct AttnPlan {
 
 namespace {
 
-__device__ __align__(64) const uint32_t zero_row[128] = {};
-
 template <typename T> struct Mma;
 template <> struct Mma<Bf16> {
     static __device__ __forceinline__ f32x16 m32(bf16x8 a, bf16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
@@ -64,14 +62,6 @@ template <> struct Mma<F16> {
     static __device__ __forceinline__ f32x16 m32(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
     static __device__ __forceinline__ f32x4 m16(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 };
-
-// 16 bytes per lane from g to LDS at lds + 16 * lane.  In asm so that the
-// compiler does not make every LDS read wait for it; the caller waits.
-__device__ __forceinline__ void dma16(const char* g, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(g) : "memory");
-}
-
-__device__ __forceinline__ void wait_all() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 
 // Maximum / sum over the lanes that hold one row: l ^ 32, and l ^ 16 for 16 rows.
 template <int R>
