@@ -1,13 +1,21 @@
 // Rejected drafts out of the cache, and the cache cut to a budget.
 //
 // A first kernel, one workgroup per (sequence, key head), finds which tokens
-// stay.  Scores become 32-bit keys in the same order (a recent token takes
-// the highest key, NaN that of -inf); the key of the last token that stays is
-// found bit by bit from the top, counting the tokens at or above each trial
-// key.  Then one walk over the slots in order settles ties (the lowest slots
-// first) and pairs the free slots below the new length with the kept tokens
-// above it.  Sources are all at or above the new length and destinations all
-// below it, so a second kernel moves K and V rows in any order.
+// stay.  Scores become 32-bit keys in the same order (a recent token takes the
+// highest key, NaN that of -inf).  The key of the last token that stays is
+// found 8 bits at a time from the top, by a histogram of the tokens that share
+// the bits found so far; each of its 256 counters has 32 copies, one per LDS
+// bank, because scores cluster (a handful of exponents) and equal addresses of
+// one LDS add run one after the other.  Positions and keys are read once and
+// stay in registers (up to 32 per thread; longer sequences are read again at
+// each pass).  Ties go to the lowest slots, and the free slots below the new
+// length are paired in order with the kept tokens above it: a wave owns a run
+// of slots, so three joins of the waves' counts give every rank.
+//
+// Sources are all at or above the new length and destinations all below it, so
+// a second kernel moves K and V rows in any order.  It is bound by memory
+// (4.1 TB/s of reads and writes at 117 MB, a plain copy reaches 5.1); the first
+// by its passes: few workgroups, one per head.
 #include <math.h>
 
 #include "bnn_device.hpp"
@@ -25,128 +33,210 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ int wave_sum(int v) {
-#pragma unroll
-    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m, 64);
-    return v;
-}
-
-// Sum over the workgroup, the same in every thread.  part: EV / 64 words.
-__device__ __forceinline__ int block_sum(int v, int* part) {
-    v = wave_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-    __syncthreads();
-    int s = 0;
-#pragma unroll
-    for (int i = 0; i < EV / 64; ++i) s += part[i];
-    return s;
-}
-
-__device__ __forceinline__ int block_max(int v, int* part) {
-#pragma unroll
-    for (int m = 32; m; m >>= 1) { const int o = __shfl_xor(v, m, 64); v = o > v ? o : v; }
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-    __syncthreads();
-    int s = part[0];
-#pragma unroll
-    for (int i = 1; i < EV / 64; ++i) s = part[i] > s ? part[i] : s;
-    return s;
-}
-
-// Number of threads before this one whose flag is set, and the total.
-__device__ __forceinline__ int block_rank(bool flag, int* part, int& total) {
-    const uint64_t m = __ballot(flag);
+// This wave's share joined with the others': the sum of the waves before it,
+// and of all.  part: EV / 64 words of its own.
+__device__ __forceinline__ int before_wave(int v, int* part, int& total) {
     const int w = threadIdx.x >> 6;
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) part[w] = __popcll(m);
+    if ((threadIdx.x & 63) == 0) part[w] = v;
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
     for (int i = 0; i < EV / 64; ++i) { before += i < w ? part[i] : 0; all += part[i]; }
     total = all;
-    return before + __popcll(m & ((1ull << (threadIdx.x & 63)) - 1));
+    return before;
 }
 
-__global__ __launch_bounds__(EV) void k_evict_select(KvCache c, KvBatch b, EvictArgs a) {
-    __shared__ int part[EV / 64];
-    const int kh = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x;
-    const Seq sq = sequence(c, b, seq);
+struct EvictLds {
+    uint32_t hist[256 * 32];
+    uint32_t bins[256];
+    int part[6][EV / 64];
+};
+
+// The highest of all threads' values.
+__device__ __forceinline__ void block_max(int& last, EvictLds& lds) {
+#pragma unroll
+    for (int m = 32; m; m >>= 1) { const int o = __shfl_xor(last, m, 64); last = o > last ? o : last; }
+    if ((threadIdx.x & 63) == 0) lds.part[1][threadIdx.x >> 6] = last;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < EV / 64; ++i) last = lds.part[1][i] > last ? lds.part[1][i] : last;
+}
+
+// KPT: slots per thread that stay in registers; 0: any number, read again.
+template <int KPT>
+__device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& a, const Seq& sq, int seq, int kh, EvictLds& lds) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t at = ((int64_t)seq * c.kv_heads + kh) * a.ld_slots;
-    const float* score = a.score_in + at;
-    const int32_t* pos = a.pos_in + at;
-    auto valid = [&](int s) {
+    const float* const score = a.score_in + at;
+    const int32_t* const pos = a.pos_in + at;
+    const int steps = (sq.total + EV - 1) / EV;     // of 64 slots, for each wave
+    const int first = wave * steps * 64 + lane;     // this thread's slots: first + 64 i
+    auto valid_at = [&](int s) {
         return s < sq.ctx || (s < sq.total && (!a.accept || packed_bit(a.accept + seq * a.ld_accept, a.ld_accept, s - sq.ctx)));
     };
+    constexpr int N = KPT ? KPT : 1;
+    const int mine = (wave + 1) * steps * 64 < sq.total ? (wave + 1) * steps * 64 : sq.total;   // end of the wave's slots
+    uint32_t key[N], valid = 0;   // valid: bit i for slot first + 64 i
     int n = 0, last = INT32_MIN;
-    for (int s = tid; s < sq.total; s += EV)
-        if (valid(s)) { ++n; last = pos[s] > last ? pos[s] : last; }
-    n = block_sum(n, part);
-    last = block_max(last, part);
+    if constexpr (KPT > 0) {
+        int32_t p[N];
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const int s = first + 64 * i, in = s < mine ? s : 0;   // a lane past the end reads a slot that is there
+            p[i] = sq.total ? pos[in] : 0;
+            key[i] = __float_as_uint(sq.total ? score[in] : 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const int s = first + 64 * i;
+            bool v = s < mine;
+            if (__any(v && s >= sq.ctx)) v = v && valid_at(s);
+            valid |= (uint32_t)v << i;
+            n += __popcll(__ballot(v));
+            last = v && p[i] > last ? p[i] : last;
+        }
+        block_max(last, lds);
+        const int64_t since = (int64_t)last - a.recent;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) key[i] = p[i] > since ? 0xFFFFFFFFu : score_key(__uint_as_float(key[i]));
+    } else {
+        for (int i = 0; i < steps; ++i) {
+            const int s = first + 64 * i;
+            const bool v = valid_at(s);
+            n += __popcll(__ballot(v));
+            if (v) last = pos[s] > last ? pos[s] : last;
+        }
+        block_max(last, lds);
+    }
+    int all;
+    before_wave(n, lds.part[0], all);
+    n = all;
     const int keep = n < a.budget ? n : a.budget;
     const int64_t since = (int64_t)last - a.recent;
-    auto key = [&](int s) { return pos[s] > since ? 0xFFFFFFFFu : score_key(score[s]); };
+    const int low = keep < mine ? keep : mine;   // this wave's slots below the new length end here
+    // f(i, slot, valid, key) for this thread's slots, every thread of a wave alike
+    auto each = [&](auto f) {
+        if constexpr (KPT > 0) {
+#pragma unroll
+            for (int i = 0; i < KPT; ++i)
+                f(i, first + 64 * i, (valid >> i & 1u) != 0, key[i]);
+        } else {
+            for (int i = 0; i < steps; ++i) {
+                const int s = first + 64 * i;
+                const bool v = valid_at(s);
+                f(i, s, v, !v ? 0u : pos[s] > since ? 0xFFFFFFFFu : score_key(score[s]));
+            }
+        }
+    };
 
-    // the largest key that at least keep tokens reach
+    // the largest key that at least keep tokens reach, and how many of its tokens stay
     uint32_t edge = 0;
-    int above = 0;   // tokens above it
-    if (keep < n && keep > 0) {
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t trial = edge | (1u << bit);
-            int cnt = 0;
-            for (int s = tid; s < sq.total; s += EV) cnt += valid(s) && key(s) >= trial;
-            cnt = block_sum(cnt, part);
-            if (cnt >= keep) edge = trial;
+    int ties = keep;
+    const bool cut = keep < n && keep > 0;
+    if (cut) {
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            for (int i = tid; i < 256 * 32; i += EV) lds.hist[i] = 0;
+            __syncthreads();
+            each([&](int, int, bool v, uint32_t k) {
+                if (v && (shift == 24 || k >> ((shift + 8) & 31) == edge >> ((shift + 8) & 31)))
+                    atomicAdd(&lds.hist[(k >> shift & 255u) * 32 + (lane & 31)], 1u);
+            });
+            __syncthreads();
+            {   // four threads per counter, eight copies each
+                const int bin = tid >> 2;
+                uint32_t t = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t += lds.hist[bin * 32 + (tid & 3) * 8 + ((j + bin) & 7)];
+                t += __shfl_xor(t, 1, 64);
+                t += __shfl_xor(t, 2, 64);
+                if ((tid & 3) == 0) lds.bins[bin] = t;
+            }
+            __syncthreads();
+            // from the top: each lane takes four counters, lane 0 the highest
+            uint32_t b4[4], mine = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) { b4[j] = lds.bins[255 - 4 * lane - j]; mine += b4[j]; }
+            uint32_t upto = mine;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) { const uint32_t o = __shfl_up(upto, m, 64); upto += lane >= m ? o : 0u; }
+            const int hit = __ffsll((unsigned long long)__ballot(upto >= (uint32_t)ties)) - 1;   // ties >= 1: some lane
+            uint32_t above = upto - mine, digit = 0;
+            bool found = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (!found && above + b4[j] >= (uint32_t)ties) { found = true; digit = 255 - 4 * lane - j; }
+                if (!found) above += b4[j];
+            }
+            edge |= (uint32_t)__builtin_amdgcn_readlane(digit, hit) << shift;
+            ties -= __builtin_amdgcn_readlane(above, hit);
         }
-        int cnt = 0;
-        for (int s = tid; s < sq.total; s += EV) cnt += valid(s) && key(s) > edge;
-        above = block_sum(cnt, part);
     }
-    const int ties = keep - above;   // of the tokens at the edge, the first ones
 
-    int32_t* work = a.work + ((int64_t)seq * c.kv_heads + kh) * evict_work_words(c.capacity);
-    int32_t* from = work + 16;
-    int32_t* to = from + evict_work_words(c.capacity) / 2 - 8;
-    int tied = 0, holes = 0, movers = 0;
-    for (int s0 = 0; s0 < sq.total; s0 += EV) {
-        const int s = s0 + tid;
-        bool kept = valid(s);
-        bool tie = false;
-        if (kept && keep < n) {
-            const uint32_t k = keep > 0 ? key(s) : 0;
-            tie = keep > 0 && k == edge;
-            kept = keep > 0 && k > edge;
-        }
-        int count;
-        const int r = block_rank(tie, part, count);
-        kept = kept || (tie && tied + r < ties);
-        tied += count;
-        const bool hole = s < keep && !kept, mover = s >= keep && kept;
-        const int rh = block_rank(hole, part, count);
-        if (hole) to[holes + rh] = s;
-        holes += count;
-        const int rm = block_rank(mover, part, count);
-        if (mover) from[movers + rm] = s;
-        movers += count;
+    // which stay: bit i of a word per thread, or again where they are not in registers
+    int tied = 0;
+    if (cut) {
+        int t = 0;
+        each([&](int, int, bool v, uint32_t k) { t += __popcll(__ballot(v && k == edge)); });
+        tied = before_wave(t, lds.part[2], all);
+    }
+    const uint64_t below = (1ull << lane) - 1;
+    auto stays = [&](bool v, uint32_t k, int& tie) {
+        if (!cut) return v && keep > 0;
+        const uint64_t m = __ballot(v && k == edge);
+        const bool s = v && (k > edge || (k == edge && tie + __popcll(m & below) < ties));
+        tie += __popcll(m);
+        return s;
+    };
+    int holes = 0, movers = 0;
+    uint32_t kept = 0;
+    {
+        int tie = tied;
+        each([&](int i, int s, bool v, uint32_t k) {
+            const bool st = stays(v, k, tie);
+            if (KPT) kept |= (uint32_t)st << i;
+            holes += __popcll(__ballot(s < low && !st));
+            movers += __popcll(__ballot(s >= keep && st));
+        });
+    }
+    const int hole0 = before_wave(holes, lds.part[3], all), mover0 = before_wave(movers, lds.part[4], all);
+    int32_t* const work = a.work + ((int64_t)seq * c.kv_heads + kh) * evict_work_words(c.capacity);
+    int32_t* const from = work + 16;
+    int32_t* const to = from + evict_work_words(c.capacity) / 2 - 8;
+    {
+        int tie = tied, h = hole0, m = mover0;
+        each([&](int i, int s, bool v, uint32_t k) {
+            const bool st = KPT ? (kept >> i & 1u) != 0 : stays(v, k, tie);
+            const bool hole = s < low && !st, mover = s >= keep && st;
+            const uint64_t hm = __ballot(hole), mm = __ballot(mover);
+            if (hole) to[h + __popcll(hm & below)] = s;
+            if (mover) from[m + __popcll(mm & below)] = s;
+            h += __popcll(hm);
+            m += __popcll(mm);
+            if (s < keep && st && a.pos_out != a.pos_in) a.pos_out[at + s] = pos[s];
+            if (s < keep && st && a.score_out != a.score_in) a.score_out[at + s] = score[s];
+        });
     }
     __syncthreads();
-    __threadfence_block();
-    for (int s = tid; s < keep; s += EV) {
-        a.pos_out[at + s] = pos[s];
-        a.score_out[at + s] = score[s];
-    }
-    __syncthreads();
-    for (int i = tid; i < movers; i += EV) {
-        a.pos_out[at + to[i]] = pos[from[i]];
-        a.score_out[at + to[i]] = score[from[i]];
+    for (int i = tid; i < all; i += EV) {
+        const int f = from[i], t = to[i];
+        a.pos_out[at + t] = pos[f];
+        a.score_out[at + t] = score[f];
     }
     __syncthreads();
     for (int s = keep + tid; s < sq.total; s += EV) {
         a.pos_out[at + s] = -1;
         a.score_out[at + s] = 0.f;
     }
-    if (tid == 0) { work[0] = movers; work[1] = keep; }
+    if (tid == 0) { work[0] = all; work[1] = keep; }
+}
+
+template <int KPT>
+__global__ __launch_bounds__(EV) void k_evict_select(KvCache c, KvBatch b, EvictArgs a) {
+    __shared__ EvictLds lds;
+    const int kh = blockIdx.x, seq = blockIdx.y;
+    const Seq sq = sequence(c, b, seq);
+    if (sq.total <= EV * KPT) evict_select<KPT>(c, a, sq, seq, kh, lds);
+    else evict_select<0>(c, a, sq, seq, kh, lds);
 }
 
 __global__ __launch_bounds__(256) void k_evict_move(KvCache c, EvictArgs a) {
@@ -171,10 +261,14 @@ __global__ __launch_bounds__(256) void k_evict_move(KvCache c, EvictArgs a) {
 }  // namespace
 
 hipError_t launch_cache_evict(const KvCache& c, const KvBatch& b, const EvictArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(k_evict_select, dim3(c.kv_heads, b.B), dim3(EV), 0, s, c, b, a);
+    const int64_t rows = (int64_t)b.max_ctx + b.max_nodes;
+    const dim3 heads(c.kv_heads, b.B);
+    if (rows <= 4 * EV) hipLaunchKernelGGL((k_evict_select<4>), heads, dim3(EV), 0, s, c, b, a);
+    else if (rows <= 8 * EV) hipLaunchKernelGGL((k_evict_select<8>), heads, dim3(EV), 0, s, c, b, a);
+    else if (rows <= 16 * EV) hipLaunchKernelGGL((k_evict_select<16>), heads, dim3(EV), 0, s, c, b, a);
+    else hipLaunchKernelGGL((k_evict_select<32>), heads, dim3(EV), 0, s, c, b, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t rows = (int64_t)b.max_ctx + b.max_nodes;
     int64_t most = a.budget < rows ? a.budget : rows;   // moves of a head
     if (rows - most < most && rows - most > 0) most = rows - most;
     int64_t blocks = (most * (c.dim / 8) + 255) / 256;
