@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -620,6 +621,26 @@ def pack_weights_ternary(W: torch.Tensor, *, gamma: torch.Tensor | None = None, 
 
 
 # ---- the decoder's key/value cache
+#
+# These calls take a few microseconds on the GPU for a single token, so the
+# argument structs are packed in one go (the layouts of the ctypes classes
+# above) and the checks test what is right first.
+
+def _layout(struct_type) -> struct.Struct:
+    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
+    s = struct.Struct("@" + "".join(codes[t] for _, t in struct_type._fields_))
+    last, _ = struct_type._fields_[-1]
+    assert s.size == getattr(struct_type, last).offset + getattr(struct_type, last).size
+    return s
+
+
+_pack_batch, _pack_rope, _pack_attn, _pack_score, _pack_evict = (
+    _layout(t).pack for t in (_KvBatch, _RopeArgs, _AttnArgs, _ScoreArgs, _EvictArgs))
+
+
+def _raw_stream(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
 
 BF16, F16, F32 = 1, 2, 3
 _KV_TYPES = {torch.bfloat16: BF16, torch.float16: F16}
@@ -671,30 +692,44 @@ class KVCache:
         return t
 
 
-def _batch(cache: KVCache, indptr, ctx, rows: int, max_nodes: int, max_ctx: int) -> _KvBatch:
-    b = _KvBatch()
-    _dev(indptr, torch.int32, "indptr")
-    _dev(ctx, torch.int32, "ctx")
+def _batch(cache: KVCache, indptr, ctx, rows: int, max_nodes: int, max_ctx: int) -> bytes:
     n = ctx.numel()
-    if indptr.numel() != n + 1 or n > cache.sequences or not indptr.is_contiguous() or not ctx.is_contiguous():
+    if not (indptr.dtype is torch.int32 and ctx.dtype is torch.int32 and indptr.is_cuda and ctx.is_cuda and indptr.numel() == n + 1
+            and n <= cache.sequences and indptr.is_contiguous() and ctx.is_contiguous()):
+        _dev(indptr, torch.int32, "indptr")
+        _dev(ctx, torch.int32, "ctx")
         raise ValueError("indptr must be [B + 1] and ctx [B], contiguous, for at most the cache's sequences")
-    b.indptr, b.ctx, b.B, b.rows = indptr.data_ptr(), ctx.data_ptr(), n, rows
-    b.max_nodes, b.max_ctx = max_nodes, max_ctx
-    return b
+    return _pack_batch(indptr.data_ptr(), ctx.data_ptr(), n, rows, max_nodes, max_ctx)
 
 
-def _token_rows(t: torch.Tensor, dtype, name: str, rows, heads, dim) -> torch.Tensor:
-    _dev(t, dtype, name)
-    if t.dim() != 3 or t.stride(2) != 1 or t.shape[0] != rows or t.shape[1] != heads or t.shape[2] != dim:
+def _token_rows(t: torch.Tensor, dtype, name: str, rows, heads, dim):
+    """Address, row stride and head stride of a token tensor."""
+    st = t.stride()
+    if not (t.dtype is dtype and t.is_cuda and t.shape == (rows, heads, dim) and st[2] == 1):
+        _dev(t, dtype, name)
         raise ValueError(f"{name} must be [{rows}, {heads}, {dim}] with a unit last stride (got {tuple(t.shape)})")
-    return t
+    return t.data_ptr(), st[0], st[1]
+
+
+def _flat(t: torch.Tensor, dtype, name: str, n: int) -> int:
+    if not (t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous()):
+        _dev(t, dtype, name)
+        raise ValueError(f"{name} must be contiguous, with {n} elements")
+    return t.data_ptr()
+
+
+def _row_floats(t: torch.Tensor, name: str, rows: int, heads: int):
+    if not (t.dtype is torch.float32 and t.is_cuda and t.shape == (rows, heads) and t.stride(1) == 1):
+        _dev(t, torch.float32, name)
+        raise ValueError(f"{name} must be [{rows}, {heads}] with a unit last stride")
+    return t.data_ptr(), t.stride(0)
 
 
 def _bit_rows(t: torch.Tensor | None, name: str, rows: int):
     if t is None:
-        return None, 0
-    _dev(t, torch.int32, name)
-    if t.dim() != 2 or t.shape[0] != rows or not t.is_contiguous():
+        return 0, 0
+    if not (t.dtype is torch.int32 and t.is_cuda and t.dim() == 2 and t.shape[0] == rows and t.is_contiguous()):
+        _dev(t, torch.int32, name)
         raise ValueError(f"{name} must be a contiguous packed int32 [{rows}, words] tensor")
     return t.data_ptr(), t.shape[1]
 
@@ -744,44 +779,30 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCac
     src = q.dtype
     if src is not torch.float32 and src is not cache.dtype:
         raise TypeError(f"q must be torch.float32 or {cache.dtype} (got {src})")
-    _token_rows(q, src, "q", rows, heads, cache.dim)
-    _token_rows(k, src, "k", rows, cache.kv_heads, cache.dim)
-    _token_rows(v, src, "v", rows, cache.kv_heads, cache.dim)
-    _dev(positions, torch.int32, "positions")
-    if positions.numel() != rows or not positions.is_contiguous():
-        raise ValueError("positions must be a contiguous [rows] tensor")
-    b = _batch(cache, indptr, ctx, rows, rows, 0)
+    dim = cache.dim
+    kv = cache.kv_heads
     if q_out is None:
         q_out = torch.empty((rows, heads, dim), dtype=cache.dtype, device=q.device)
-    else:
-        _token_rows(q_out, cache.dtype, "q_out", rows, heads, dim)
-    a = _RopeArgs()
-    a.q, a.q_row, a.q_head = q.data_ptr(), q.stride(0), q.stride(1)
-    a.k, a.k_row, a.k_head = k.data_ptr(), k.stride(0), k.stride(1)
-    a.v, a.v_row, a.v_head = v.data_ptr(), v.stride(0), v.stride(1)
-    a.src_dtype = F32 if src is torch.float32 else _KV_TYPES[src]
-    a.heads = heads
-    a.q_out, a.qo_row, a.qo_head = q_out.data_ptr(), q_out.stride(0), q_out.stride(1)
-    a.positions = positions.data_ptr()
+    table, max_pos, rot = 0, 0, 0
     if turns is not None:
-        _dev(turns, torch.float32, "turns")
-        if turns.dim() != 2 or not turns.is_contiguous():
+        if turns.dim() != 2:
             raise ValueError("turns must be a contiguous [max_pos, rot] tensor")
-        a.turns, a.max_pos, a.rot = turns.data_ptr(), turns.shape[0], turns.shape[1]
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _dev(w, torch.float32, name)
-            if w.numel() != dim or not w.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous [{dim}] tensor")
-            setattr(a, name, w.data_ptr())
-    a.interleaved, a.eps = int(bool(interleaved)), eps
+        max_pos, rot = turns.shape
+        table = _flat(turns, torch.float32, "turns", max_pos * rot)
+    pos, score, slots = 0, 0, 0
     if cache.pos is not None:
-        a.pos, a.ld_slots = cache.pos.data_ptr(), cache.pos.shape[2]
+        pos, slots = cache.pos.data_ptr(), cache.pos.shape[2]
     if cache.score is not None:
-        if cache.pos is not None and cache.pos.shape[2] != cache.score.shape[2]:
+        if pos and slots != cache.score.shape[2]:
             raise ValueError("cache.pos and cache.score must have the same number of slots")
-        a.score, a.ld_slots = cache.score.data_ptr(), cache.score.shape[2]
-    _check(lib().bnn_qk_norm_rope(cache._ref, ctypes.addressof(b), ctypes.addressof(a), _stream(q.device)),
+        score, slots = cache.score.data_ptr(), cache.score.shape[2]
+    a = _pack_rope(*_token_rows(q, src, "q", rows, heads, dim), *_token_rows(k, src, "k", rows, kv, dim),
+                   *_token_rows(v, src, "v", rows, kv, dim), F32 if src is torch.float32 else _KV_TYPES[src], heads,
+                   *_token_rows(q_out, cache.dtype, "q_out", rows, heads, dim),
+                   _flat(positions, torch.int32, "positions", rows), table, max_pos, rot, 1 if interleaved else 0,
+                   0 if q_weight is None else _flat(q_weight, torch.float32, "q_weight", dim),
+                   0 if k_weight is None else _flat(k_weight, torch.float32, "k_weight", dim), eps, pos, score, slots)
+    _check((_lib or lib()).bnn_qk_norm_rope(cache._ref, _batch(cache, indptr, ctx, rows, rows, 0), a, _raw_stream(q.device)),
            "bnn_qk_norm_rope")
     return q_out
 
@@ -789,9 +810,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCac
 def tree_attention_workspace(cache: KVCache, rows: int, heads: int, max_nodes: int, max_ctx: int) -> torch.Tensor:
     """A workspace for tree_attention calls of up to these sizes over this
     cache's sequences."""
-    b = _KvBatch()
-    b.B, b.rows, b.max_nodes, b.max_ctx = cache.sequences, rows, max_nodes, max_ctx
-    n = lib().bnn_tree_attention_workspace(cache._ref, ctypes.addressof(b), heads)
+    b = _pack_batch(0, 0, cache.sequences, rows, max_nodes, max_ctx)
+    n = lib().bnn_tree_attention_workspace(cache._ref, b, heads)
     if n < 0:
         raise ValueError("tree_attention_workspace: sizes out of range")
     return torch.empty(n, dtype=torch.uint8, device=cache.device)
@@ -809,32 +829,22 @@ def tree_attention(q: torch.Tensor, cache: KVCache, indptr: torch.Tensor, ctx: t
     (out [rows, heads, dim] in ``out_dtype``: float32, or the cache's type by
     default; lse float32 [rows, heads], the logarithm of each row's sum)."""
     rows, heads, dim = q.shape
-    _token_rows(q, cache.dtype, "q", rows, heads, cache.dim)
     b = _batch(cache, indptr, ctx, rows, max_nodes, max_ctx)
     if out is None:
         out = torch.empty((rows, heads, dim), dtype=out_dtype or cache.dtype, device=q.device)
-    else:
-        _token_rows(out, out.dtype, "out", rows, heads, dim)
-    if out.dtype is not torch.float32 and out.dtype is not cache.dtype:
-        raise TypeError(f"out must be torch.float32 or {cache.dtype} (got {out.dtype})")
     if lse is None:
         lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
-    _dev(lse, torch.float32, "lse")
-    if lse.shape != (rows, heads):
-        raise ValueError(f"lse must be [{rows}, {heads}]")
+    kind = out.dtype
+    if kind is not torch.float32 and kind is not cache.dtype:
+        raise TypeError(f"out must be torch.float32 or {cache.dtype} (got {kind})")
+    L = _lib or lib()
     if workspace is None:
-        workspace = torch.empty(max(0, lib().bnn_tree_attention_workspace(cache._ref, ctypes.addressof(b), heads)),
-                                dtype=torch.uint8, device=q.device)
-    a = _AttnArgs()
-    a.q, a.q_row, a.q_head, a.heads = q.data_ptr(), q.stride(0), q.stride(1), heads
-    a.mask, a.ld_mask = _bit_rows(mask, "mask", rows)
-    a.scale = dim ** -0.5 if scale is None else scale
-    a.out, a.o_row, a.o_head = out.data_ptr(), out.stride(0), out.stride(1)
-    a.out_dtype = F32 if out.dtype is torch.float32 else _KV_TYPES[out.dtype]
-    a.lse, a.ld_lse = lse.data_ptr(), _ld(lse)
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(lib().bnn_tree_attention(cache._ref, ctypes.addressof(b), ctypes.addressof(a), _stream(q.device)),
-           "bnn_tree_attention")
+        workspace = torch.empty(max(0, L.bnn_tree_attention_workspace(cache._ref, b, heads)), dtype=torch.uint8, device=q.device)
+    a = _pack_attn(*_token_rows(q, cache.dtype, "q", rows, heads, cache.dim), heads, *_bit_rows(mask, "mask", rows),
+                   dim ** -0.5 if scale is None else scale, *_token_rows(out, kind, "out", rows, heads, dim),
+                   F32 if kind is torch.float32 else _KV_TYPES[kind], *_row_floats(lse, "lse", rows, heads),
+                   workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(L.bnn_tree_attention(cache._ref, b, a, _raw_stream(q.device)), "bnn_tree_attention")
     return out, lse
 
 
@@ -847,25 +857,16 @@ def cache_score_add(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, indptr: 
     ``accept``: packed int32 [B, words], None where all tokens count.  Writes
     the sums in place, or into ``score_out``, and returns them."""
     rows, heads, dim = q.shape
-    _token_rows(q, cache.dtype, "q", rows, heads, cache.dim)
     if cache.score is None:
         raise ValueError("the cache has no score tensor")
-    b = _batch(cache, indptr, ctx, rows, max_nodes, max_ctx)
-    _dev(lse, torch.float32, "lse")
-    if lse.shape != (rows, heads):
-        raise ValueError(f"lse must be [{rows}, {heads}]")
     if score_out is None:
         score_out = cache.score
     elif _dev(score_out, torch.float32, "score_out").shape != cache.score.shape or not score_out.is_contiguous():
         raise ValueError("score_out must be laid out as cache.score")
-    a = _ScoreArgs()
-    a.q, a.q_row, a.q_head, a.heads = q.data_ptr(), q.stride(0), q.stride(1), heads
-    a.lse, a.ld_lse = lse.data_ptr(), _ld(lse)
-    a.mask, a.ld_mask = _bit_rows(mask, "mask", rows)
-    a.accept, a.ld_accept = _bit_rows(accept, "accept", b.B)
-    a.scale = dim ** -0.5 if scale is None else scale
-    a.score_in, a.score_out, a.ld_slots = cache.score.data_ptr(), score_out.data_ptr(), cache.score.shape[2]
-    _check(lib().bnn_cache_score_add(cache._ref, ctypes.addressof(b), ctypes.addressof(a), _stream(q.device)),
+    a = _pack_score(*_token_rows(q, cache.dtype, "q", rows, heads, cache.dim), heads, *_row_floats(lse, "lse", rows, heads),
+                    *_bit_rows(mask, "mask", rows), *_bit_rows(accept, "accept", ctx.numel()), dim ** -0.5 if scale is None else scale,
+                    cache.score.data_ptr(), score_out.data_ptr(), cache.score.shape[2])
+    _check((_lib or lib()).bnn_cache_score_add(cache._ref, _batch(cache, indptr, ctx, rows, max_nodes, max_ctx), a, _raw_stream(q.device)),
            "bnn_cache_score_add")
     return score_out
 
@@ -891,25 +892,19 @@ def cache_evict(cache: KVCache, indptr: torch.Tensor, ctx: torch.Tensor, *, budg
         raise ValueError("the cache has no pos or no score tensor")
     if cache.pos.shape != cache.score.shape:
         raise ValueError("cache.pos and cache.score must have the same shape")
-    b = _batch(cache, indptr, ctx, 1 << 30, max_nodes, max_ctx)
     pos_out = cache.pos if pos_out is None else _dev(pos_out, torch.int32, "pos_out")
     score_out = cache.score if score_out is None else _dev(score_out, torch.float32, "score_out")
     ctx_out = ctx if ctx_out is None else _dev(ctx_out, torch.int32, "ctx_out")
-    for t in (pos_out, score_out):
-        if t.shape != cache.pos.shape or not t.is_contiguous():
-            raise ValueError("pos_out and score_out must be laid out as cache.pos")
+    slots = cache.pos.shape
+    if pos_out.shape != slots or score_out.shape != slots or not (pos_out.is_contiguous() and score_out.is_contiguous()):
+        raise ValueError("pos_out and score_out must be laid out as cache.pos")
     if ctx_out.shape != ctx.shape or not ctx_out.is_contiguous():
         raise ValueError("ctx_out must be laid out as ctx")
     if workspace is None:
         workspace = cache_evict_workspace(cache)
-    a = _EvictArgs()
-    a.accept, a.ld_accept = _bit_rows(accept, "accept", b.B)
-    a.budget, a.recent = budget, recent
-    a.pos_in, a.pos_out = cache.pos.data_ptr(), pos_out.data_ptr()
-    a.score_in, a.score_out = cache.score.data_ptr(), score_out.data_ptr()
-    a.ld_slots = cache.pos.shape[2]
-    a.ctx_out = ctx_out.data_ptr()
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(lib().bnn_cache_evict(cache._ref, ctypes.addressof(b), ctypes.addressof(a), _stream(cache.device)),
+    a = _pack_evict(*_bit_rows(accept, "accept", ctx.numel()), budget, recent, cache.pos.data_ptr(), pos_out.data_ptr(),
+                    cache.score.data_ptr(), score_out.data_ptr(), slots[2], ctx_out.data_ptr(), workspace.data_ptr(),
+                    workspace.numel() * workspace.element_size())
+    _check((_lib or lib()).bnn_cache_evict(cache._ref, _batch(cache, indptr, ctx, 1 << 30, max_nodes, max_ctx), a, _raw_stream(cache.device)),
            "bnn_cache_evict")
     return ctx_out
