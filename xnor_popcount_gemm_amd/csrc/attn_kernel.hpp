@@ -19,12 +19,18 @@
 // instead of at every step.
 //
 // Tiles.  K and V rows go from global memory straight to LDS (16 bytes per
-// lane), two buffers deep: the next step's rows are in flight while one is
-// worked on.  16 slots of 32 dimensions form a 1 KiB block, slot r at 64 r
-// bytes, its four 16-byte pieces permuted by XOR so that the 8 lanes served
-// together read different banks: by (r >> 1) & 3 for K (b128 reads of one
-// piece of 8 slots), by 2 ((r >> 1) & 1) for V (transposed reads of two
-// pieces of 4 slots).  Rows past the end are read from a block of zeros.
+// lane); the next step's rows are in flight while one is worked on, in a
+// second buffer where the waves of a workgroup share the tile.  With up to 32
+// rows each wave has tiles of its own, which pass on to registers so that one
+// buffer will do and twice the waves fit a compute unit.  A wave's load brings 1 KiB: 8 rows of 128 bytes, whole cache lines
+// (16 rows of 64 bytes for 96 dimensions).  Where one row tile reads them,
+// without keeping them in the caches: 64 sequences of about 6200 slots take
+// 285 us by whole lines that way (5.6 TB/s) and 311 kept; in half lines 396
+// and 327.  The 16-byte pieces of row r are
+// permuted by XOR so that the lanes served together read different banks: by
+// r % 8 for K (b128 reads of one piece of 8 slots), by 2 (r % 4) for V
+// (transposed reads of two pieces of 4 slots).  Rows past the end are read
+// from a block of zeros.
 //
 // Masks.  Committed slots are seen by every row and cost nothing; the steps
 // that hold new tokens run in a loop of their own and take one 32-bit word per
@@ -109,10 +115,19 @@ struct Attn {
     static constexpr int GRP = 32 * D;                          // bytes of 16 slots
     static constexpr int VOFF = BN * D * 2;                     // V after K in a buffer
     static constexpr int STAGE = 2 * VOFF;
-    static constexpr int GROUP_LDS = 2 * STAGE;                 // two buffers of a slot group
+    static constexpr bool REGS = RW == 1;                       // tiles pass through registers: one buffer
+    static constexpr bool ONCE = REGS && Block16<D, true>::WIDE;         // one row tile reads K and V, by whole lines
+    static constexpr int KR = R == 32 ? QS : 2 * QS;            // operands of a 32-slot tile of K; of V as many
+    static constexpr int GROUP_LDS = (REGS ? 1 : 2) * STAGE;    // buffers of a slot group
     static constexpr int OPAD = D + 4;
     static constexpr int MERGE = KW > 1 ? KW * RW * R * OPAD * 4 + KW * RW * R * 8 : 4 * 32 * 36 * 4;
     static constexpr int LDS = KW * GROUP_LDS > MERGE ? KW * GROUP_LDS : MERGE;
+    typedef Block16<D, RW == 1> B;
+    static constexpr int PIECES = B::PIECES, HALVES = B::HALVES, COLS = B::COLS;
+    // reads of one operand that differ in more than a constant offset
+    static constexpr int KV = R == 32 ? PIECES / 2 : PIECES / 4, VV = R == 32 ? PIECES / 4 : PIECES / 2;
+    static constexpr int VSTEP = R == 16 ? GRP : B::WIDE ? COLS * 1024 : 512;   // to the other 4 slots of an operand
+
     // 16-slot groups that a wave fetches per step, and whether it fetches both K and V of them
     static constexpr int FETCH = RW == 1 ? 2 : 1;
     static constexpr bool SPLIT_KV = RW == 4 && BN == 32;
@@ -124,7 +139,7 @@ struct Attn {
     static __device__ __forceinline__ vec8 v_frag(const char* base, int o) {
         typedef __attribute__((address_space(3))) s16x4* tp;
         const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tp)(base + o));
-        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tp)(base + o + (R == 32 ? 512 : GRP)));
+        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tp)(base + o + VSTEP));
         return __builtin_bit_cast(vec8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     }
 
@@ -198,21 +213,20 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
         }
     }
 
-    // fetch of K and V rows: a lane takes 16-byte pieces of slot lane / 4 of a 16-slot group
+    // fetch of K and V rows: a lane takes 16-byte pieces of one row per block
     char* const my = lds + kw * A::GROUP_LDS;
     const uint32_t my_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)my;
-    const int fr = lane >> 2;
-    const int kpiece = ((lane & 3) ^ ((fr >> 1) & 3)) * 16, vpiece = ((lane & 3) ^ (2 * ((fr >> 1) & 1))) * 16;
-    const char* const kbase = c.K + kh * c.k_head + kpiece;
-    const char* const vbase = c.V + kh * c.v_head + vpiece;
+    const int fr = lane / A::PIECES, fp = lane % A::PIECES;   // row (of the first block) and place in it
+    const char* const kbase = c.K + kh * c.k_head + (fp ^ A::B::k_swap(fr)) * 16;
+    const char* const vbase = c.V + kh * c.v_head + (fp ^ A::B::v_swap(fr)) * 16;
     const int32_t* const table = c.table ? c.table + (int64_t)seq * c.ld_table : nullptr;
-    int32_t entry[A::FETCH];
-    uint32_t place[A::FETCH];
+    int32_t entry[A::FETCH * A::HALVES];
+    uint32_t place[A::FETCH * A::HALVES];
     auto lookup = [&](int step) {
 #pragma unroll
-        for (int f = 0; f < A::FETCH; ++f) {
-            const int g = RW == 1 ? f : rw % (A::BN / 16);
-            const int slot = k0 + (step * KW + kw) * A::BN + 16 * g + fr;
+        for (int f = 0; f < A::FETCH * A::HALVES; ++f) {
+            const int g = RW == 1 ? f / A::HALVES : rw % (A::BN / 16);
+            const int slot = k0 + (step * KW + kw) * A::BN + 16 * g + 8 * (f % A::HALVES) + fr;
             entry[f] = -1;
             if (slot < k1) {
                 const uint32_t p = fastdiv(slot, c.page);
@@ -223,39 +237,37 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
     };
     auto fetch = [&](int buf) {
 #pragma unroll
-        for (int f = 0; f < A::FETCH; ++f) {
-            const int g = RW == 1 ? f : rw % (A::BN / 16);
+        for (int f = 0; f < A::FETCH * A::HALVES; ++f) {
+            const int g = RW == 1 ? f / A::HALVES : rw % (A::BN / 16);
             const bool there = (uint32_t)entry[f] < c.num_pages;
-            const uint32_t to = my_lds + buf * A::STAGE + g * A::GRP;
+            const uint32_t to = my_lds + buf * A::STAGE + g * A::GRP + (f % A::HALVES) * A::COLS * 1024;
             if (!A::SPLIT_KV || rw < 2) {
                 const char* p = there ? kbase + entry[f] * c.k_page + place[f] * c.k_slot : (const char*)zero_row;
 #pragma unroll
-                for (int j = 0; j < D / 32; ++j) dma16(p + 64 * j, to + 1024 * j);
+                for (int j = 0; j < A::COLS; ++j) A::ONCE ? dma16_once(p + 16 * A::PIECES * j, to + 1024 * j) : dma16(p + 16 * A::PIECES * j, to + 1024 * j);
             }
             if (!A::SPLIT_KV || rw >= 2) {
                 const char* p = there ? vbase + entry[f] * c.v_page + place[f] * c.v_slot : (const char*)zero_row;
 #pragma unroll
-                for (int j = 0; j < D / 32; ++j) dma16(p + 64 * j, to + A::VOFF + 1024 * j);
+                for (int j = 0; j < A::COLS; ++j) A::ONCE ? dma16_once(p + 16 * A::PIECES * j, to + A::VOFF + 1024 * j) : dma16(p + 16 * A::PIECES * j, to + A::VOFF + 1024 * j);
             }
         }
     };
 
-    // LDS offsets of this lane's operand reads
-    int kread[2], vread[2];
+    // LDS offsets of this lane's operand reads: read q of K is kread[q % KV] + q / KV KiB, block i of V alike
+    int kread[A::KV], vread[A::VV];
     if constexpr (R == 32) {
-        const int s = lane & 15, hi = lane >> 5, z = (s >> 1) & 3;
-        const int base = ((lane >> 4) & 1) * A::GRP + s * 64;
-        kread[0] = base + ((hi ^ z) * 16);
-        kread[1] = base + (((2 + hi) ^ z) * 16);
-        const int i = lane & 15, d = (lane >> 4) & 1, key = 4 * hi + (i >> 2);
-        vread[0] = A::VOFF + key * 64 + (((2 * d + ((i & 3) >> 1)) ^ (2 * ((key >> 1) & 1))) * 16) + (i & 1) * 8;
-        vread[1] = vread[0];
+        const int r = lane & 15, hi = lane >> 5, d = (lane >> 4) & 1, key = 4 * hi + (r >> 2);
+#pragma unroll
+        for (int q = 0; q < A::KV; ++q) kread[q] = d * A::GRP + A::B::place_of(r, 2 * q + hi, A::B::k_swap(r));
+#pragma unroll
+        for (int i = 0; i < A::VV; ++i) vread[i] = A::VOFF + A::B::place_of(key, 4 * i + 2 * d + ((r & 3) >> 1), A::B::v_swap(key)) + (r & 1) * 8;
     } else {
-        const int s = lane & 15, quad = lane >> 4, z = (s >> 1) & 3;
-        kread[0] = kread[1] = s * 64 + ((quad ^ z) * 16);
-        const int key = 4 * quad + (s >> 2), zv = 2 * ((key >> 1) & 1);
-        vread[0] = A::VOFF + key * 64 + ((((s & 3) >> 1) ^ zv) * 16) + (s & 1) * 8;
-        vread[1] = A::VOFF + key * 64 + (((2 + ((s & 3) >> 1)) ^ zv) * 16) + (s & 1) * 8;
+        const int r = lane & 15, quad = lane >> 4, key = 4 * quad + (r >> 2);
+#pragma unroll
+        for (int q = 0; q < A::KV; ++q) kread[q] = A::B::place_of(r, 4 * q + quad, A::B::k_swap(r));
+#pragma unroll
+        for (int i = 0; i < A::VV; ++i) vread[i] = A::VOFF + A::B::place_of(key, 2 * i + ((r & 3) >> 1), A::B::v_swap(key)) + (r & 1) * 8;
     }
 
     acc o[A::OB];
@@ -267,83 +279,97 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
 #pragma unroll
     for (int i = 0; i < A::PW; ++i) plus[i] = minus[i] = 0;
 
-    // one step: BN slots from kb0 on, in the buffer buf
-    auto work = [&](auto is_masked, const char* buf, const int kb0) {
+    // one step: BN slots from kb0 on, in the buffer buf; with kr, vr their operands already in registers
+    auto work = [&](auto is_masked, const char* buf, const int kb0, const vec8* kr, const vec8* vr) {
         constexpr bool MASKED = decltype(is_masked)::value;
+        constexpr bool REGS = A::REGS && !MASKED;
+        uint32_t vis[A::SUB];
+        if (MASKED) {
+            bool any = false;
 #pragma unroll
-        for (int sub = 0; sub < A::SUB; ++sub) {
-            const int kb = kb0 + 32 * sub;
-            uint32_t vis = 0xFFFFFFFFu;
-            if (MASKED) {
-                if (kb >= k1) break;
-                const int rel = kb - sq.ctx;
+            for (int sub = 0; sub < A::SUB; ++sub) {
+                const int kb = kb0 + 32 * sub, rel = kb - sq.ctx;
+                uint32_t v = 0xFFFFFFFFu;
                 if (live && rel > -32) {
                     if (!a.mask) {
                         const int n = node - rel + 1;
-                        vis = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+                        v = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
                     } else {
                         const uint32_t* mr = a.mask + row * a.ld_mask;
                         if (rel >= 0) {
                             const int w = rel >> 5;
                             const uint64_t lo = w < a.ld_mask ? mr[w] : 0u, hi = w + 1 < a.ld_mask ? mr[w + 1] : 0u;
-                            vis = (uint32_t)((lo | hi << 32) >> (rel & 31));
+                            v = (uint32_t)((lo | hi << 32) >> (rel & 31));
                         } else {
-                            vis = (mr[0] << -rel) | ((1u << -rel) - 1);
+                            v = (mr[0] << -rel) | ((1u << -rel) - 1);
                         }
                     }
                 }
-                if (k1 - kb < 32) vis &= (1u << (k1 - kb)) - 1;
-                if (!__any(live && vis != 0)) continue;
+                if (k1 - kb < 32) v &= k1 > kb ? (1u << (k1 - kb)) - 1 : 0u;
+                vis[sub] = v;
+                any |= live && v != 0;
             }
+            if (!__any(any)) return;
+        }
 
-            // scores
-            float sc[A::NSC];
+        // scores
+        float sc[A::SUB][A::NSC];
+#pragma unroll
+        for (int sub = 0; sub < A::SUB; ++sub) {
             if constexpr (R == 32) {
                 f32x16 s = {};
 #pragma unroll
                 for (int q = 0; q < A::QS; ++q)
-                    s = Mma<T>::m32(*(const vec8*)(buf + sub * 2 * A::GRP + kread[q & 1] + (q >> 1) * 1024), qf[q], s);
+                    s = Mma<T>::m32(REGS ? kr[q] : *(const vec8*)(buf + sub * 2 * A::GRP + kread[q % A::KV] + q / A::KV * 1024), qf[q], s);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sc[i] = s[i];
+                for (int i = 0; i < 16; ++i) sc[sub][i] = s[i];
             } else {
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     f32x4 s = {};
 #pragma unroll
                     for (int q = 0; q < A::QS; ++q)
-                        s = Mma<T>::m16(*(const vec8*)(buf + g * A::GRP + kread[0] + q * 1024), qf[q], s);
+                        s = Mma<T>::m16(REGS ? kr[g * A::QS + q] : *(const vec8*)(buf + g * A::GRP + kread[q % A::KV] + q / A::KV * 1024), qf[q], s);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[4 * g + i] = s[i];
+                    for (int i = 0; i < 4; ++i) sc[sub][4 * g + i] = s[i];
                 }
             }
-            if (MASKED) {
+        }
+        if (MASKED) {
 #pragma unroll
-                for (int i = 0; i < A::NSC; ++i) sc[i] = (vis >> A::slot_of(i, lane)) & 1u ? sc[i] : -INFINITY;
+            for (int sub = 0; sub < A::SUB; ++sub)
+#pragma unroll
+                for (int i = 0; i < A::NSC; ++i) sc[sub][i] = (vis[sub] >> A::slot_of(i, lane)) & 1u ? sc[sub][i] : -INFINITY;
+        }
+        float mx = sc[0][0];
+#pragma unroll
+        for (int sub = 0; sub < A::SUB; ++sub)
+#pragma unroll
+            for (int i = 0; i < A::NSC; ++i) mx = fmaxf(mx, sc[sub][i]);
+        mx = row_max<R>(mx) * c2;
+        if (__any(mx > m + 8.f)) {
+            const float mn = fmaxf(m, mx);
+            const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < A::OB; ++i) o[i] *= f;
+        }
+        const float ms = m == -INFINITY ? 0.f : m;
+        float ls[2] = {0.f, 0.f};
+#pragma unroll
+        for (int sub = 0; sub < A::SUB; ++sub)
+#pragma unroll
+            for (int i = 0; i < A::NSC; ++i) {
+                float p = __builtin_amdgcn_exp2f(fmaf(sc[sub][i], c2, -ms));
+                if (MASKED) p = (vis[sub] >> A::slot_of(i, lane)) & 1u ? p : 0.f;   // a scale of 0 makes NaN of an unseen one's -inf
+                sc[sub][i] = p;
+                ls[i & 1] += p;
             }
-            float mx = sc[0];
-#pragma unroll
-            for (int i = 1; i < A::NSC; ++i) mx = fmaxf(mx, sc[i]);
-            mx = row_max<R>(mx) * c2;
-            if (__any(mx > m + 8.f)) {
-                const float mn = fmaxf(m, mx);
-                const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
-                m = mn;
-                l *= f;
-#pragma unroll
-                for (int i = 0; i < A::OB; ++i) o[i] *= f;
-            }
-            const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll
-            for (int i = 0; i < A::NSC; ++i) sc[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], c2, -ms));
-            if (MASKED) {   // a scale of 0 makes NaN of the unseen ones' -inf
-#pragma unroll
-                for (int i = 0; i < A::NSC; ++i) sc[i] = (vis >> A::slot_of(i, lane)) & 1u ? sc[i] : 0.f;
-            }
-            float ls = 0.f;
-#pragma unroll
-            for (int i = 0; i < A::NSC; ++i) ls += sc[i];
-            l += ls;
+        l += ls[0] + ls[1];
 
+#pragma unroll
+        for (int sub = 0; sub < A::SUB; ++sub) {
             // weights as 16-bit operands: one term, or as many as keep them whole
             vec8 pf[A::NSC / 8][NS];
 #pragma unroll
@@ -352,9 +378,9 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
                 for (int n = 0; n < NS; ++n)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const typename A::elem p = (typename A::elem)sc[8 * g + i];
+                        const typename A::elem p = (typename A::elem)sc[sub][8 * g + i];
                         pf[g][n][i] = p;
-                        if (n + 1 < NS) sc[8 * g + i] -= (float)p;
+                        if (n + 1 < NS) sc[sub][8 * g + i] -= (float)p;
                     }
             }
             const char* vb = buf + sub * 2 * A::GRP;
@@ -362,8 +388,8 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
             for (int g = 0; g < A::NSC / 8; ++g)
 #pragma unroll
                 for (int i = 0; i < A::OB; ++i) {
-                    vec8 v = R == 32 ? A::v_frag(vb, vread[0] + g * A::GRP + i * 1024)
-                                     : A::v_frag(vb, vread[i & 1] + (i >> 1) * 1024);
+                    vec8 v = REGS ? vr[g * A::OB + i]
+                           : A::v_frag(vb, vread[i % A::VV] + i / A::VV * 1024 + (R == 32 ? g * A::GRP : 0));
                     if (MASKED) v = A::finite(v);
 #pragma unroll
                     for (int n = 0; n < NS; ++n) o[i] = A::mma(v, pf[g][n], o[i]);
@@ -379,9 +405,8 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
                 if (__any(bad)) {   // rare: slot by slot
 #pragma unroll 1
                     for (int key = 0; key < 32; ++key) {
-                        const bool saw = (vis >> key) & 1u;
-                        const char* vr = vb + A::VOFF + (key >> 4) * A::GRP + (key & 15) * 64;
-                        const int z = 2 * ((key >> 1) & 1);
+                        const bool saw = (vis[sub] >> key) & 1u;
+                        const char* vr = vb + A::VOFF + (key >> 4) * A::GRP;
 #pragma unroll
                         for (int w = 0; w < A::PW; ++w) {
                             uint32_t up = 0, down = 0;
@@ -390,7 +415,7 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
                                 const int piece = 8 * w + q;   // 4 dimensions of this lane's row
                                 if (piece >= A::OB * (R == 32 ? 4 : 1)) break;
                                 const int d = R == 32 ? 8 * piece + 4 * (lane >> 5) : 16 * piece + 4 * (lane >> 4);
-                                const u32x2 x = *(const u32x2*)(vr + (d >> 5) * 1024 + ((((d >> 3) & 3) ^ z) * 16) + (d & 4) * 2);
+                                const u32x2 x = *(const u32x2*)(vr + A::B::place_of(key & 15, d >> 3, A::B::v_swap(key & 15)) + (d & 4) * 2);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     const uint32_t h = (e < 2 ? x[0] : x[1]) >> (16 * (e & 1)) & 0xFFFFu;
@@ -417,23 +442,61 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
         fetch(0);
         if (steps > 1) lookup(1);
     }
-    auto next = [&](int st) {   // step st is in LDS; the next one is on its way
-        wait_all();
-        if (RW > 1) __builtin_amdgcn_s_barrier();
-        if (st + 1 < steps) {
-            fetch((st + 1) & 1);
-            if (st + 2 < steps) lookup(st + 2);
-        }
-        return my + (st & 1) * A::STAGE;
-    };
     int st = 0;
-    for (; st < plain; ++st) {
-        const char* buf = next(st);
-        work(std::false_type{}, buf, k0 + (st * KW + kw) * A::BN);
-    }
-    for (; st < steps; ++st) {
-        const char* buf = next(st);
-        work(std::true_type{}, buf, k0 + (st * KW + kw) * A::BN);
+    if constexpr (A::REGS) {
+        // a wave's own tile: once it is in registers, the next one comes to the same place
+        vec8 kr[A::KR], vr[A::KR];
+        for (; st < plain; ++st) {
+            wait_all();
+            if constexpr (R == 32) {
+#pragma unroll
+                for (int q = 0; q < A::QS; ++q) kr[q] = *(const vec8*)(my + kread[q % A::KV] + q / A::KV * 1024);
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int i = 0; i < A::OB; ++i) vr[g * A::OB + i] = A::v_frag(my, vread[i % A::VV] + i / A::VV * 1024 + g * A::GRP);
+            } else {
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int q = 0; q < A::QS; ++q) kr[g * A::QS + q] = *(const vec8*)(my + g * A::GRP + kread[q % A::KV] + q / A::KV * 1024);
+#pragma unroll
+                for (int i = 0; i < A::OB; ++i) vr[i] = A::v_frag(my, vread[i % A::VV] + i / A::VV * 1024);
+            }
+            wait_lds();
+            if (st + 1 < steps) {
+                fetch(0);
+                if (st + 2 < steps) lookup(st + 2);
+            }
+            work(std::false_type{}, my, k0 + (st * KW + kw) * A::BN, kr, vr);
+        }
+        for (; st < steps; ++st) {
+            wait_all();
+            work(std::true_type{}, my, k0 + (st * KW + kw) * A::BN, nullptr, nullptr);
+            wait_lds();
+            if (st + 1 < steps) {
+                fetch(0);
+                if (st + 2 < steps) lookup(st + 2);
+            }
+        }
+    } else {
+        auto next = [&](int st) {   // step st is in LDS; the next one is on its way
+            wait_all();
+            if (RW > 1) __builtin_amdgcn_s_barrier();
+            if (st + 1 < steps) {
+                fetch((st + 1) & 1);
+                if (st + 2 < steps) lookup(st + 2);
+            }
+            return my + (st & 1) * A::STAGE;
+        };
+        for (; st < plain; ++st) {
+            const char* buf = next(st);
+            work(std::false_type{}, buf, k0 + (st * KW + kw) * A::BN, nullptr, nullptr);
+        }
+        for (; st < steps; ++st) {
+            const char* buf = next(st);
+            work(std::true_type{}, buf, k0 + (st * KW + kw) * A::BN, nullptr, nullptr);
+        }
     }
     {
         uint32_t any = 0;
@@ -544,33 +607,59 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
     }
 }
 
-// Joins the chunks of the rows whose sequence was cut.  D / 4 lanes per (row, head).
+// Joins the chunks of the rows whose sequence was cut.  A wave per (row, head):
+// a lane per chunk for the weights, then D / 4 lanes per row, 64 / (D / 4) rows
+// at a time.
 template <int D, typename O>
 __global__ __launch_bounds__(256) void k_join_chunks(KvCache c, KvBatch b, AttnArgs a, AttnPlan pl) {
-    constexpr int PER = D / 4, ROWS = 256 / PER;
-    const int row = blockIdx.x, tid = threadIdx.x;
-    const int seq = row_sequence(b, row, tid & 63);
-    if (seq < 0) return;
+    constexpr int PER = D / 4, PARTS = 64 / PER;
+    const int row = blockIdx.x, lane = threadIdx.x & 63;
+    const int h = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int seq = row_sequence(b, row, lane);
+    if (seq < 0 || h >= a.heads) return;
     const Seq sq = sequence(c, b, seq);
     int nchunk = (sq.total + pl.chunk - 1) / pl.chunk;
     nchunk = nchunk > pl.chunks ? pl.chunks : nchunk;
     if (nchunk <= 1 || row - sq.row0 >= b.max_nodes) return;
-    const int h = blockIdx.y * ROWS + tid / PER, d = (tid % PER) * 4;
-    if (tid / PER >= ROWS || h >= a.heads) return;
-    const int64_t prow = part_rows(b.rows, a.heads);
-    const float* pout = (const float*)a.work;
-    const float2* pml = (const float2*)(a.work + (int64_t)pl.chunks * prow * D * 4);
-    const int64_t at = (int64_t)row * a.heads + h;
+    const int64_t prow = part_rows(b.rows, a.heads), at = (int64_t)row * a.heads + h;
+    const float* const pout = (const float*)a.work + at * D;
+    const float2* const pml = (const float2*)(a.work + (int64_t)pl.chunks * prow * D * 4) + at;
+    const int part = lane / PER, d = (lane % PER) * 4;
     float M = -INFINITY, l = 0.f;
-    for (int k = 0; k < nchunk; ++k) M = fmaxf(M, pml[k * prow + at].x);
     f32x4 y = {0, 0, 0, 0};
-    for (int k = 0; k < nchunk; ++k) {
-        const float2 x = pml[k * prow + at];
-        if (x.x == -INFINITY) continue;
-        const float f = __builtin_amdgcn_exp2f(x.x - M);
-        l += x.y * f;
-        y += *(const f32x4*)(pout + (k * prow + at) * D + d) * f;
+    for (int k0 = 0; k0 < nchunk; k0 += 64) {
+        float2 x = make_float2(-INFINITY, 0.f);
+        if (k0 + lane < nchunk) x = pml[(k0 + lane) * prow];
+        float top = x.x;
+#pragma unroll
+        for (int t = 32; t; t >>= 1) top = fmaxf(top, __shfl_xor(top, t, 64));
+        const float Mn = fmaxf(M, top);
+        if (Mn == -INFINITY) continue;   // nothing seen so far
+        const float f = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x.x - Mn);
+        float ls = x.y * f;
+        if (f == 0.f) ls = 0.f;
+#pragma unroll
+        for (int t = 32; t; t >>= 1) ls += __shfl_xor(ls, t, 64);
+        const float keep = M == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(M - Mn);
+        l = l * keep + ls;
+        y *= keep;
+        M = Mn;
+        const int n = nchunk - k0 < 64 ? nchunk - k0 : 64;
+#pragma unroll 4
+        for (int kb = 0; kb < n; kb += PARTS) {   // every lane takes every turn: the weights are lane reads
+            const int k = kb + part;
+            const float w = __shfl(f, k & 63, 64);   // 0 where the chunk holds nothing for this row, whatever its memory
+            f32x4 v = {0, 0, 0, 0};
+            if (k < n) v = *(const f32x4*)(pout + (int64_t)(k0 + k) * prow * D + d);
+            if (k < n && w != 0.f) y += v * w;
+        }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (PARTS >= 2) y[i] += __shfl(y[i], (lane + PER) & 63, 64);
+        if (PARTS == 4) y[i] += __shfl(y[i], (lane + 2 * PER) & 63, 64);
+    }
+    if (part != 0) return;
     y *= l == 0.f ? 0.f : 1.f / l;
     typedef O ov __attribute__((ext_vector_type(4)));
     *(ov*)(a.out + row * a.o_row + h * a.o_head + d * sizeof(O)) = __builtin_convertvector(y, ov);
@@ -592,8 +681,7 @@ hipError_t launch_dim(const KvCache& c, const KvBatch& b, const AttnArgs& a, con
     else launch_tiles<T, D, 32, 4, 1, NS, O>(c, b, a, pl, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || pl.chunks == 1) return e;
-    constexpr int ROWS = 256 / (D / 4);
-    hipLaunchKernelGGL((k_join_chunks<D, O>), dim3(b.rows, (a.heads + ROWS - 1) / ROWS), dim3(256), 0, s, c, b, a, pl);
+    hipLaunchKernelGGL((k_join_chunks<D, O>), dim3(b.rows, (a.heads + 3) / 4), dim3(256), 0, s, c, b, a, pl);
     return hipGetLastError();
 }
 

@@ -108,13 +108,34 @@ __device__ __forceinline__ void dma16(const char* g, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(g) : "memory");
 }
 
-// The same for rows that nobody reads again soon: 7.0 TB/s instead of 6.2 over
-// 400 MB.
+// The same, not kept in the caches: for rows that are read once, and only by
+// whole 128-byte lines (half lines came from memory twice).
 __device__ __forceinline__ void dma16_once(const char* g, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" :: "s"(lds), "v"(g) : "memory");
 }
 
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void wait_all() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+
+// K or V rows of 16 slots in LDS, as loads of 1 KiB per wave bring them: blocks
+// of 8 rows of 128 bytes (LINES, if the dimensions are a multiple of 64), or 16
+// rows of 64.  Whole lines are needed to read past the caches; half lines take
+// half the page lookups per lane.
+// Piece c (8 dimensions) of row r lies at place_of(r, c, swap), its place in
+// the row permuted by the XOR of k_swap(r) or v_swap(r).
+template <int D, bool LINES>
+struct Block16 {
+    static constexpr bool WIDE = LINES && D % 64 == 0;
+    static constexpr int PIECES = WIDE ? 8 : 4;      // of a row in a block
+    static constexpr int HALVES = WIDE ? 2 : 1;      // blocks over the 16 rows
+    static constexpr int COLS = D / 8 / PIECES;      // blocks over a row
+    static __host__ __device__ constexpr int k_swap(int r) { return WIDE ? r & 7 : (r >> 1) & 3; }
+    static __host__ __device__ constexpr int v_swap(int r) { return WIDE ? 2 * (r & 3) : 2 * ((r >> 1) & 1); }
+    static __device__ __forceinline__ int place_of(int r, int c, int swap) {
+        const int half = WIDE ? r >> 3 : 0, in = WIDE ? r & 7 : r;
+        return (half * COLS + c / PIECES) * 1024 + in * (16 * PIECES) + ((c % PIECES) ^ swap) * 16;
+    }
+};
 
 struct Bf16 {
     typedef __bf16 elem;

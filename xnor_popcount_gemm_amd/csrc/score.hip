@@ -5,7 +5,7 @@
 //             of exp(scale <q_ig, k_j> - lse_ig)
 //
 // Bound by the read of K.  A wave works on 32 slots at a time: their K rows go
-// straight to LDS (4 lanes fetch 64 bytes of a row), from there to registers,
+// straight to LDS (8 lanes fetch a line of 128 bytes), from there to registers,
 // as the second operand of S = Q K^T in 16x16x32 matrix products, and the next
 // 32 rows are on their way to the same LDS while these are worked on.  Up to
 // 32 accepted rows (new tokens times query heads of the group) stay in LDS
@@ -60,9 +60,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, quad = lane >> 4;
-    const int fr = lane >> 2;
+    typedef Block16<D, true> B;
+    constexpr int KV = B::PIECES / 4;      // reads of K that differ in more than a constant offset
+    const int fr = lane / B::PIECES;       // row this lane fetches of a block, and of a Q block
+    const int qr = lane >> 2;
     const uint32_t my_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds[wave];
-    const char* const kread = lds[wave] + col * 64 + ((quad ^ ((col >> 1) & 3)) * 16);
+    const char* const qread = lds[wave] + 2 * GRP + col * 64 + ((quad ^ ((col >> 1) & 3)) * 16);
+    const char* kread[KV];
+#pragma unroll
+    for (int i = 0; i < KV; ++i) kread[i] = lds[wave] + B::place_of(col, 4 * i + quad, B::k_swap(col));
     const float c2 = a.scale * 1.44269504088896340736f;
     const bool copies = a.out != a.in;
     const int64_t waves = (int64_t)gridDim.x * 4, me = (int64_t)blockIdx.x * 4 + wave;
@@ -108,13 +114,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
         const int run = (int)(left < mine - tile ? left : mine - tile);
         const int end = tile + run;
         const int32_t* const table = c.table ? c.table + (int64_t)seq * c.ld_table : nullptr;
-        // a lane fetches piece lane % 4 of rows lane / 4, permuted so that the reads spread over the banks
-        const char* const kbase = c.K + kh * c.k_head + ((lane & 3) ^ ((fr >> 1) & 3)) * 16;
+        const char* const kbase = c.K + kh * c.k_head + ((lane % B::PIECES) ^ B::k_swap(fr)) * 16;
         // page entries: 64 of the table at a time, one per lane, so that a tile's lookups are lane reads
         const int64_t pages = table ? c.ld_table : 0;
         int32_t held = -1;
         int64_t held0 = -64;
-        const char* ptr[NB];
+        const char* ptr[NB * B::HALVES];
         auto locate = [&](int t) {   // the rows of tile t
             const uint32_t first_page = fastdiv((uint32_t)t * 32, c.page);
             uint32_t last_slot = (uint32_t)t * 32 + 31;
@@ -125,8 +130,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
                 asm volatile("" : "+v"(held));   // waited for here: at its use the wait would take in the rows on their way
             }
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const uint32_t slot = (uint32_t)t * 32 + 16 * n + fr, pg = fastdiv(slot, c.page);
+            for (int n = 0; n < NB * B::HALVES; ++n) {
+                const uint32_t slot = (uint32_t)t * 32 + 16 / B::HALVES * n + fr, pg = fastdiv(slot, c.page);
                 const uint32_t place = slot - pg * c.page.d;
                 int32_t entry = seq;
                 if (table) entry = __shfl(held, (int)(pg - held0), 64);
@@ -136,9 +141,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
         };
         auto fetch = [&] {
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int n = 0; n < NB * B::HALVES; ++n)
 #pragma unroll
-                for (int s = 0; s < QS; ++s) dma16_once(ptr[n] + 64 * s, my_lds + n * GRP + 1024 * s);
+                for (int s = 0; s < B::COLS; ++s) {
+                    const char* p = ptr[n] + 16 * B::PIECES * s;
+                    const uint32_t to = my_lds + (n * B::COLS + s) * 1024;
+                    B::WIDE ? dma16_once(p, to) : dma16(p, to);   // read once; half lines would come twice
+                }
         };
         auto before = [&](int t) {   // lanes 0 .. 31 write a slot each
             const int64_t slot = (int64_t)t * 32 + lane;
@@ -157,19 +166,19 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
         auto stage = [&](int r0, int rows) {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const int r = r0 + 16 * g + fr;
+                const int r = r0 + 16 * g + qr;
                 const bool live = r < rows;
                 const int rank = live ? r / a.group : 0;
                 const int node = taken[wave][rank];
                 const int64_t row = sq.row0 + node;
                 const int head = kh * a.group + (live ? r - rank * a.group : 0);
-                const char* q = live ? a.q + row * a.q_row + head * a.q_head + ((lane & 3) ^ ((fr >> 1) & 3)) * 16 : (const char*)zero_row;
+                const char* q = live ? a.q + row * a.q_row + head * a.q_head + ((lane & 3) ^ ((qr >> 1) & 3)) * 16 : (const char*)zero_row;
 #pragma unroll
                 for (int s = 0; s < QS; ++s) dma16(q + 64 * s, my_lds + (2 + g) * GRP + 1024 * s);
                 if ((lane & 3) == 0) {
                     const float lse = live ? a.lse[row * a.ld_lse + head] * 1.44269504088896340736f : INFINITY;
-                    lows[wave][16 * g + fr] = lse == -INFINITY ? INFINITY : lse;
-                    node_of[wave][16 * g + fr] = live ? node : -1;
+                    lows[wave][16 * g + qr] = lse == -INFINITY ? INFINITY : lse;
+                    node_of[wave][16 * g + qr] = live ? node : -1;
                 }
             }
         };
@@ -217,7 +226,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int s = 0; s < QS; ++s) k[n][s] = *(const vec8*)(kread + n * GRP + 1024 * s);
+                    for (int s = 0; s < QS; ++s) k[n][s] = *(const vec8*)(kread[s % KV] + n * GRP + s / KV * 1024);
                 const float old = next;
                 const int64_t s0 = (int64_t)t * 32;
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before it is overwritten
@@ -245,7 +254,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
                             f32x4 x[NB] = {};
 #pragma unroll
                             for (int s = 0; s < QS; ++s) {
-                                const vec8 q = *(const vec8*)(kread + (2 + g) * GRP + 1024 * s);
+                                const vec8 q = *(const vec8*)(qread + g * GRP + 1024 * s);
 #pragma unroll
                                 for (int n = 0; n < NB; ++n) x[n] = mma16(q, k[n][s], x[n]);
                             }
