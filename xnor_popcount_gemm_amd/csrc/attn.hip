@@ -33,6 +33,8 @@ AttnPlan make_plan(int32_t dim, int32_t kv_heads, const KvBatch& b, int32_t head
     p.chunk = (int32_t)chunk;
     p.chunks = (int32_t)((slots + chunk - 1) / chunk);
     if (p.chunks < 1) p.chunks = 1;
+    const int64_t groups = (int64_t)b.B * kv_heads * p.chunks;
+    p.groups = groups < 0x7FFFFFFF / 16 && (groups + 8) * tiles < 0x7FFFFFFF ? (int32_t)groups : -1;   // -1: past one launch
     return p;
 }
 
@@ -40,7 +42,7 @@ AttnPlan make_plan(int32_t dim, int32_t kv_heads, const KvBatch& b, int32_t head
 
 int64_t tree_attention_work(int32_t dim, int32_t kv_heads, const KvBatch& b, int32_t heads) {
     const AttnPlan p = make_plan(dim, kv_heads, b, heads);
-    if ((int64_t)p.chunks * p.row_tiles > INT32_MAX) return -1;
+    if (p.groups < 0) return -1;
     return p.chunks == 1 ? 0 : (int64_t)p.chunks * b.rows * heads * (dim * 4 + 8);
 }
 

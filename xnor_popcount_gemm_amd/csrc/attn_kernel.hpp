@@ -32,11 +32,11 @@
 // (transposed reads of two pieces of 4 slots).  Rows past the end are read
 // from a block of zeros.
 //
-// Masks.  Committed slots are seen by every row and cost nothing; the steps
-// that hold new tokens run in a loop of their own and take one 32-bit word per
-// row and 32 slots.  An unseen token must not matter even where its V is NaN
-// or infinite, and 0 * NaN is NaN, so that loop takes such values as 0 in the
-// products and notes, as bits per row and dimension, which rows saw an
+// Masks.  Committed slots are seen by every row and cost nothing; steps that
+// hold new tokens take one 32-bit word per row and 32 slots, and run as the
+// others do where every row sees them whole (a causal run below its diagonal).  An unseen token must not matter even where its V is NaN
+// or infinite, and 0 * NaN is NaN, so a masked step takes such values as 0 in
+// the products and notes, as bits per row and dimension, which rows saw an
 // infinity of which sign (NaN: both); the infinities are added at the end.
 #pragma once
 
@@ -55,6 +55,7 @@ struct AttnPlan {
     int32_t row_tiles;     // of a (sequence, key head), at most
     int32_t chunk;         // slots per workgroup
     int32_t chunks;        // of a sequence, at most
+    int32_t groups;        // chunks of all sequences and key heads
 };
 
 namespace {
@@ -174,7 +175,11 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int rw = wave % RW, kw = wave / RW;
-    const int rt = blockIdx.x / pl.chunks, ci = blockIdx.x % pl.chunks, kh = blockIdx.y, seq = blockIdx.z;
+    // Workgroups go to the 8 XCDs in turn, and each XCD has its own L2: the row tiles of a chunk of a key head,
+    // which read the same K and V, take every eighth place.
+    const uint32_t idx = blockIdx.x / 8, group = idx / pl.row_tiles * 8 + blockIdx.x % 8;
+    if (group >= (uint32_t)pl.groups) return;
+    const int rt = idx % pl.row_tiles, ci = group % pl.chunks, pair = group / pl.chunks, kh = pair % c.kv_heads, seq = pair / c.kv_heads;
 
     const Seq sq = sequence(c, b, seq);
     const int nodes = sq.nodes < b.max_nodes ? sq.nodes : b.max_nodes;
@@ -279,38 +284,40 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
 #pragma unroll
     for (int i = 0; i < A::PW; ++i) plus[i] = minus[i] = 0;
 
-    // one step: BN slots from kb0 on, in the buffer buf; with kr, vr their operands already in registers
-    auto work = [&](auto is_masked, const char* buf, const int kb0, const vec8* kr, const vec8* vr) {
-        constexpr bool MASKED = decltype(is_masked)::value;
-        constexpr bool REGS = A::REGS && !MASKED;
-        uint32_t vis[A::SUB];
-        if (MASKED) {
-            bool any = false;
+    // which of the 32 slots from each kb0 + 32 sub on this lane's row sees; 0: no row sees any, 2: all see all, else 1
+    auto sight = [&](const int kb0, uint32_t (&vis)[A::SUB]) {
+        bool any = false, part = false;
 #pragma unroll
-            for (int sub = 0; sub < A::SUB; ++sub) {
-                const int kb = kb0 + 32 * sub, rel = kb - sq.ctx;
-                uint32_t v = 0xFFFFFFFFu;
-                if (live && rel > -32) {
-                    if (!a.mask) {
-                        const int n = node - rel + 1;
-                        v = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+        for (int sub = 0; sub < A::SUB; ++sub) {
+            const int kb = kb0 + 32 * sub, rel = kb - sq.ctx;
+            uint32_t v = 0xFFFFFFFFu;
+            if (live && rel > -32) {
+                if (!a.mask) {
+                    const int n = node - rel + 1;
+                    v = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+                } else {
+                    const uint32_t* mr = a.mask + row * a.ld_mask;
+                    if (rel >= 0) {
+                        const int w = rel >> 5;
+                        const uint64_t lo = w < a.ld_mask ? mr[w] : 0u, hi = w + 1 < a.ld_mask ? mr[w + 1] : 0u;
+                        v = (uint32_t)((lo | hi << 32) >> (rel & 31));
                     } else {
-                        const uint32_t* mr = a.mask + row * a.ld_mask;
-                        if (rel >= 0) {
-                            const int w = rel >> 5;
-                            const uint64_t lo = w < a.ld_mask ? mr[w] : 0u, hi = w + 1 < a.ld_mask ? mr[w + 1] : 0u;
-                            v = (uint32_t)((lo | hi << 32) >> (rel & 31));
-                        } else {
-                            v = (mr[0] << -rel) | ((1u << -rel) - 1);
-                        }
+                        v = (mr[0] << -rel) | ((1u << -rel) - 1);
                     }
                 }
-                if (k1 - kb < 32) v &= k1 > kb ? (1u << (k1 - kb)) - 1 : 0u;
-                vis[sub] = v;
-                any |= live && v != 0;
             }
-            if (!__any(any)) return;
+            if (k1 - kb < 32) v &= k1 > kb ? (1u << (k1 - kb)) - 1 : 0u;
+            vis[sub] = v;
+            any |= live && v != 0;
+            part |= v != 0xFFFFFFFFu;
         }
+        return !__any(any) ? 0 : __any(part) ? 1 : 2;
+    };
+
+    // one step: BN slots, in the buffer buf; with kr, vr their operands already in registers
+    auto work = [&](auto is_masked, const char* buf, const uint32_t (&vis)[A::SUB], const vec8* kr, const vec8* vr) {
+        constexpr bool MASKED = decltype(is_masked)::value;
+        constexpr bool REGS = A::REGS && !MASKED;
 
         // scores
         float sc[A::SUB][A::NSC];
@@ -443,6 +450,7 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
         if (steps > 1) lookup(1);
     }
     int st = 0;
+    uint32_t vis[A::SUB] = {};
     if constexpr (A::REGS) {
         // a wave's own tile: once it is in registers, the next one comes to the same place
         vec8 kr[A::KR], vr[A::KR];
@@ -468,11 +476,11 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
                 fetch(0);
                 if (st + 2 < steps) lookup(st + 2);
             }
-            work(std::false_type{}, my, k0 + (st * KW + kw) * A::BN, kr, vr);
+            work(std::false_type{}, my, vis, kr, vr);
         }
         for (; st < steps; ++st) {
             wait_all();
-            work(std::true_type{}, my, k0 + (st * KW + kw) * A::BN, nullptr, nullptr);
+            if (sight(k0 + (st * KW + kw) * A::BN, vis) != 0) work(std::true_type{}, my, vis, nullptr, nullptr);
             wait_lds();
             if (st + 1 < steps) {
                 fetch(0);
@@ -489,13 +497,16 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
             }
             return my + (st & 1) * A::STAGE;
         };
+        // two loops: in one, which also runs the masked steps, the plain steps took 10% longer
         for (; st < plain; ++st) {
             const char* buf = next(st);
-            work(std::false_type{}, buf, k0 + (st * KW + kw) * A::BN, nullptr, nullptr);
+            work(std::false_type{}, buf, vis, nullptr, nullptr);
         }
         for (; st < steps; ++st) {
             const char* buf = next(st);
-            work(std::true_type{}, buf, k0 + (st * KW + kw) * A::BN, nullptr, nullptr);
+            const int seen = sight(k0 + (st * KW + kw) * A::BN, vis);
+            if (D < 256 && seen == 2) work(std::false_type{}, buf, vis, nullptr, nullptr);   // at 256 dimensions it spills
+            else if (seen != 0) work(std::true_type{}, buf, vis, nullptr, nullptr);
         }
     }
     {
@@ -645,7 +656,7 @@ __global__ __launch_bounds__(256) void k_join_chunks(KvCache c, KvBatch b, AttnA
         y *= keep;
         M = Mn;
         const int n = nchunk - k0 < 64 ? nchunk - k0 : 64;
-#pragma unroll 4
+#pragma unroll 8
         for (int kb = 0; kb < n; kb += PARTS) {   // every lane takes every turn: the weights are lane reads
             const int k = kb + part;
             const float w = __shfl(f, k & 63, 64);   // 0 where the chunk holds nothing for this row, whatever its memory
@@ -668,7 +679,7 @@ __global__ __launch_bounds__(256) void k_join_chunks(KvCache c, KvBatch b, AttnA
 
 template <typename T, int D, int R, int RW, int KW, int NS, typename O>
 void launch_tiles(const KvCache& c, const KvBatch& b, const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
-    const dim3 grid((unsigned)(pl.chunks * pl.row_tiles), c.kv_heads, b.B);
+    const dim3 grid((unsigned)(((int64_t)pl.groups + 7) / 8 * 8 * pl.row_tiles));
     hipLaunchKernelGGL((k_tree_attention<T, D, R, RW, KW, NS, O>), grid, dim3(RW * KW * 64), 0, s, c, b, a, pl);
 }
 

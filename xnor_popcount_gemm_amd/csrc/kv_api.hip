@@ -221,7 +221,9 @@ bnn_status bnn_tree_attention(const bnn_kv_cache* cache, const bnn_kv_batch* bat
         if (a->ld_lse < a->heads) return BNN_ERR_LD;
         if (misaligned(a->lse, 4)) return BNN_ERR_ALIGN;
     }
-    BNN_TRY(check_work(a->workspace, a->workspace_bytes, bnn::tree_attention_work(c.dim, c.kv_heads, b, (int32_t)a->heads)));
+    const int64_t need = bnn::tree_attention_work(c.dim, c.kv_heads, b, (int32_t)a->heads);
+    if (need < 0) return BNN_ERR_SHAPE;   // more workgroups than a launch takes
+    BNN_TRY(check_work(a->workspace, a->workspace_bytes, need));
     if (b.rows == 0 || b.B == 0 || b.max_nodes == 0) return BNN_OK;
     bnn::AttnArgs r;
     r.q = (const char*)a->q; r.q_row = 2 * a->q_row; r.q_head = 2 * a->q_head;
