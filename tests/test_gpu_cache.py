@@ -475,3 +475,36 @@ def test_step_in_a_graph(bnn):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
     assert all(torch.equal(x, y) for x, y in zip(eager[1:], graphed[1:]))
     assert eager[0][-1][2].tolist() == [14, 28, 40]
+
+
+def test_example_path(bnn):
+    """The example's path: ternary projections around the cache calls.  Its
+    last step's attention is checked against the definition on what the cache
+    held, and the cache against what it must hold."""
+    banner("examples/decode_tree.py")
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import decode_tree
+    block, y, length = decode_tree.run(steps=30, sequences=3, hidden=256, heads=4, kv_heads=2, dim=64, budget=60, recent=16, nodes=9)
+    torch.cuda.synchronize()
+    assert y.shape == (27, 256) and y.isfinite().all()
+    ctx, pos = block.ctx.cpu().numpy(), block.cache.pos.cpu().numpy()
+    for b in range(3):
+        assert length[b] > 60 and ctx[b] == 60
+        for h in range(2):
+            held = pos[b, h, :60]
+            assert len(set(held.tolist())) == 60 and held.min() >= 0 and held.max() == length[b] - 1
+            assert set(range(length[b] - 16, length[b])) <= set(held.tolist())     # the recent positions stay
+            assert (pos[b, h, 60:] == -1).all()
+    # one more step, plain decoding: a token per sequence over what is in the cache
+    q = torch.randn((3, 4, 64), device="cuda").to(torch.bfloat16)
+    indptr = cuda_i32([0, 1, 2, 3])
+    k = torch.randn((3, 2, 64), device="cuda")
+    qr = bnn.qk_norm_rope(q.float(), k, k, block.cache, indptr, block.ctx, cuda_i32(length), block.turns)
+    out, lse = bnn.tree_attention(qr, block.cache, indptr, block.ctx, max_nodes=1, max_ctx=60, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    paged = ref.Paged.__new__(ref.Paged)
+    paged.K, paged.V, paged.table, paged.page = block.cache.k.cpu(), block.cache.v.cpu(), block.cache.table.cpu(), block.cache.page_size
+    case = (torch.bfloat16, torch.float32, 4, 2, 64, [60] * 3, [1] * 3)
+    check_attention(case, paged, qr.cpu(), None, out, lse, 64 ** -0.5)

@@ -41,10 +41,13 @@ __device__ __forceinline__ float over_rows(float s0, float s1) {
     return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
-// Number of 32-slot tiles of a sequence: none where nothing is to be added.
-__device__ __forceinline__ int tiles_of(const KvCache& c, const KvBatch& b, int s) {
+// Cost of a key head of a sequence: its 32-slot tiles, and START for the start
+// of a run and its masked tiles (so that no wave gets many short sequences one
+// after the other); nothing where nothing is to be added.
+constexpr int START = 3;
+__device__ __forceinline__ int cost_of(const KvCache& c, const KvBatch& b, int s) {
     const Seq q = sequence(c, b, s);
-    return q.nodes ? (q.total + 31) / 32 : 0;
+    return q.nodes ? (q.total + 31) / 32 + START : 0;
 }
 
 template <typename T, int D>
@@ -73,25 +76,25 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
     const bool copies = a.out != a.in;
     const int64_t waves = (int64_t)gridDim.x * 4, me = (int64_t)blockIdx.x * 4 + wave;
 
-    // this wave's share of all tiles, in the order sequence, key head, tile; 64 sequences per step
+    // this wave's share of the cost, in the order sequence, key head, tile; 64 sequences per step
     int64_t all = 0;
-    int tiles0 = 0, upto0 = 0;   // of sequence `lane`: its tiles, and those of the sequences up to it
+    int cost0 = 0, upto0 = 0;   // of sequence `lane`: its cost, and that of the sequences up to it
     for (int s0 = 0; s0 < b.B; s0 += 64) {
-        const int n = s0 + lane < b.B ? tiles_of(c, b, s0 + lane) : 0;
+        const int n = s0 + lane < b.B ? cost_of(c, b, s0 + lane) : 0;
         int upto = n;
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) { const int x = __shfl_up(upto, m, 64); upto += lane >= m ? x : 0; }
-        if (s0 == 0) { tiles0 = n; upto0 = upto; }
+        if (s0 == 0) { cost0 = n; upto0 = upto; }
         all += __builtin_amdgcn_readlane(upto, 63);   // below 2^31: 64 sequences of 2^25 tiles at most
     }
     all *= c.kv_heads;
     int64_t left = all * (me + 1) / waves - all * me / waves, skip = all * me / waves;
-    int seq = 0, mine = 0;   // the sequence of the first tile, and that sequence's tiles
+    int seq = 0, mine = 0;   // the sequence of the first unit, and its cost
     if (left > 0)
         for (int s0 = 0;; s0 += 64) {
-            int n = tiles0, upto = upto0;
+            int n = cost0, upto = upto0;
             if (s0 > 0) {
-                n = s0 + lane < b.B ? tiles_of(c, b, s0 + lane) : 0;
+                n = s0 + lane < b.B ? cost_of(c, b, s0 + lane) : 0;
                 upto = n;
 #pragma unroll
                 for (int m = 1; m < 64; m <<= 1) { const int x = __shfl_up(upto, m, 64); upto += lane >= m ? x : 0; }
@@ -105,14 +108,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
             }
             skip -= (int64_t)__builtin_amdgcn_readlane(upto, 63) * c.kv_heads;
         }
-    int kh = left > 0 ? (int)(skip / mine) : 0, tile = left > 0 ? (int)(skip % mine) : 0;
+    int kh = left > 0 ? (int)(skip / mine) : 0, unit = left > 0 ? (int)(skip % mine) : 0;
 
     while (left > 0) {
         const Seq sq = sequence(c, b, seq);
         const int nodes = sq.nodes < b.max_nodes ? sq.nodes : b.max_nodes;
         const int64_t at = ((int64_t)seq * c.kv_heads + kh) * a.ld_slots;
-        const int run = (int)(left < mine - tile ? left : mine - tile);
-        const int end = tile + run;
+        const int run = (int)(left < mine - unit ? left : mine - unit);
+        const int tile = unit > START ? unit - START : 0, end = unit + run - START;
         const int32_t* const table = c.table ? c.table + (int64_t)seq * c.ld_table : nullptr;
         const char* const kbase = c.K + kh * c.k_head + ((lane % B::PIECES) ^ B::k_swap(fr)) * 16;
         // page entries: 64 of the table at a time, one per lane, so that a tile's lookups are lane reads
@@ -211,7 +214,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
 
         const int first = list(0);
         const bool few = nodes <= 64 && first <= ROWS;   // all rows stay in LDS
-        if (few && first == 0) {                         // nothing to add
+        if (end <= tile) {                               // the start alone
+        } else if (few && first == 0) {                  // nothing to add
             if (copies)
                 for (int64_t s = (int64_t)tile * 32 + lane; s < (int64_t)end * 32 && s < sq.total; s += 64) a.out[at + s] = a.in[at + s];
         } else {
@@ -281,12 +285,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
             if (lane < 32 && slot < sq.total) a.out[at + slot] = done;
         }
         left -= run;
-        tile = end;
-        if (tile == mine) {
-            tile = 0;
+        unit += run;
+        if (unit == mine) {
+            unit = 0;
             if (++kh == c.kv_heads) {
                 kh = 0;
-                if (left > 0) do mine = tiles_of(c, b, ++seq); while (mine == 0);
+                if (left > 0) do mine = cost_of(c, b, ++seq); while (mine == 0);
             }
         }
     }
@@ -319,7 +323,7 @@ template <typename T, int D>
 void launch_one(const KvCache& c, const KvBatch& b, const ScoreArgs& a, hipStream_t s) {
     constexpr int PER_CU = D == 64 ? 4 : D == 96 ? 3 : D == 128 ? 2 : 1;   // by LDS
     const int64_t slots = (int64_t)b.max_ctx + b.max_nodes;
-    const int64_t tiles = (slots / 32 + 1) * c.kv_heads * b.B;
+    const int64_t tiles = (slots / 32 + 1 + START) * c.kv_heads * b.B;
     int64_t blocks = (tiles + 3) / 4;
     const int64_t most = (int64_t)num_cus() * PER_CU;   // what is resident at once
     if (blocks > most) blocks = most;
