@@ -181,6 +181,35 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
     if (group >= (uint32_t)pl.groups) return;
     const int rt = idx % pl.row_tiles, ci = group % pl.chunks, pair = group / pl.chunks, kh = pair % c.kv_heads, seq = pair / c.kv_heads;
 
+    const int k0 = ci * pl.chunk;
+
+    // fetch of K and V rows: a lane takes 16-byte pieces of one row per block
+    char* const my = lds + kw * A::GROUP_LDS;
+    const uint32_t my_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)my;
+    const int fr = lane / A::PIECES, fp = lane % A::PIECES;   // row (of the first block) and place in it
+    const char* const kbase = c.K + kh * c.k_head + (fp ^ A::B::k_swap(fr)) * 16;
+    const char* const vbase = c.V + kh * c.v_head + (fp ^ A::B::v_swap(fr)) * 16;
+    const int32_t* const table = c.table ? c.table + (int64_t)seq * c.ld_table : nullptr;
+    int32_t entry[A::FETCH * A::HALVES];
+    uint32_t place[A::FETCH * A::HALVES];
+    auto slot_of_fetch = [&](int step, int f) {
+        const int g = RW == 1 ? f / A::HALVES : rw % (A::BN / 16);
+        return k0 + (step * KW + kw) * A::BN + 16 * g + 8 * (f % A::HALVES) + fr;
+    };
+    auto lookup = [&](int step, int end) {
+#pragma unroll
+        for (int f = 0; f < A::FETCH * A::HALVES; ++f) {
+            const int slot = slot_of_fetch(step, f);
+            entry[f] = -1;
+            if (slot < end) {
+                const uint32_t p = fastdiv(slot, c.page);
+                place[f] = slot - p * c.page.d;
+                entry[f] = table ? table[p] : seq;
+            }
+        }
+    };
+    lookup(0, c.capacity);   // before the sequence's length is known
+
     const Seq sq = sequence(c, b, seq);
     const int nodes = sq.nodes < b.max_nodes ? sq.nodes : b.max_nodes;
     const int rows = nodes * a.group, tile0 = rt * R * RW;
@@ -192,7 +221,6 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
     const int last_row = (tile0 + R * RW < rows ? tile0 + R * RW : rows) - 1;
     int end = sq.total;
     if (!a.mask) { const int64_t own = (int64_t)sq.ctx + last_row / a.group + 1; end = own < end ? (int)own : end; }
-    const int k0 = ci * pl.chunk;
     int k1 = ci == nchunk - 1 ? end : k0 + pl.chunk;
     k1 = k1 < end ? k1 : end;
     const int steps = k1 > k0 ? (k1 - k0 + KW * A::BN - 1) / (KW * A::BN) : 0;
@@ -218,28 +246,6 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
         }
     }
 
-    // fetch of K and V rows: a lane takes 16-byte pieces of one row per block
-    char* const my = lds + kw * A::GROUP_LDS;
-    const uint32_t my_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)my;
-    const int fr = lane / A::PIECES, fp = lane % A::PIECES;   // row (of the first block) and place in it
-    const char* const kbase = c.K + kh * c.k_head + (fp ^ A::B::k_swap(fr)) * 16;
-    const char* const vbase = c.V + kh * c.v_head + (fp ^ A::B::v_swap(fr)) * 16;
-    const int32_t* const table = c.table ? c.table + (int64_t)seq * c.ld_table : nullptr;
-    int32_t entry[A::FETCH * A::HALVES];
-    uint32_t place[A::FETCH * A::HALVES];
-    auto lookup = [&](int step) {
-#pragma unroll
-        for (int f = 0; f < A::FETCH * A::HALVES; ++f) {
-            const int g = RW == 1 ? f / A::HALVES : rw % (A::BN / 16);
-            const int slot = k0 + (step * KW + kw) * A::BN + 16 * g + 8 * (f % A::HALVES) + fr;
-            entry[f] = -1;
-            if (slot < k1) {
-                const uint32_t p = fastdiv(slot, c.page);
-                place[f] = slot - p * c.page.d;
-                entry[f] = table ? table[p] : seq;
-            }
-        }
-    };
     auto fetch = [&](int buf) {
 #pragma unroll
         for (int f = 0; f < A::FETCH * A::HALVES; ++f) {
@@ -445,9 +451,11 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
     int plain = sure > k0 ? (sure - k0) / (KW * A::BN) : 0;
     plain = plain < steps ? plain : steps;
     if (steps > 0) {
-        lookup(0);
+#pragma unroll
+        for (int f = 0; f < A::FETCH * A::HALVES; ++f)
+            if (slot_of_fetch(0, f) >= k1) entry[f] = -1;
         fetch(0);
-        if (steps > 1) lookup(1);
+        if (steps > 1) lookup(1, k1);
     }
     int st = 0;
     uint32_t vis[A::SUB] = {};
@@ -474,7 +482,7 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
             wait_lds();
             if (st + 1 < steps) {
                 fetch(0);
-                if (st + 2 < steps) lookup(st + 2);
+                if (st + 2 < steps) lookup(st + 2, k1);
             }
             work(std::false_type{}, my, vis, kr, vr);
         }
@@ -484,7 +492,7 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
             wait_lds();
             if (st + 1 < steps) {
                 fetch(0);
-                if (st + 2 < steps) lookup(st + 2);
+                if (st + 2 < steps) lookup(st + 2, k1);
             }
         }
     } else {
@@ -493,7 +501,7 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
             if (RW > 1) __builtin_amdgcn_s_barrier();
             if (st + 1 < steps) {
                 fetch((st + 1) & 1);
-                if (st + 2 < steps) lookup(st + 2);
+                if (st + 2 < steps) lookup(st + 2, k1);
             }
             return my + (st & 1) * A::STAGE;
         };
@@ -620,35 +628,50 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
 
 // Joins the chunks of the rows whose sequence was cut.  A wave per (row, head):
 // a lane per chunk for the weights, then D / 4 lanes per row, 64 / (D / 4) rows
-// at a time.
-template <int D, typename O>
+// at a time.  AHEAD: up to EARLY rounds of chunks are read before it is known
+// how many there are; the lookups that tell take as long (5.2 instead of 8.4 us
+// for 32 rows of 32 chunks, but 45 instead of 15 for 32768 rows of 2: only where
+// all waves run at once).
+template <int D, typename O, bool AHEAD>
 __global__ __launch_bounds__(256) void k_join_chunks(KvCache c, KvBatch b, AttnArgs a, AttnPlan pl) {
-    constexpr int PER = D / 4, PARTS = 64 / PER;
+    constexpr int PER = D / 4, PARTS = 64 / PER, EARLY = 16;
     const int row = blockIdx.x, lane = threadIdx.x & 63;
     const int h = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int seq = row_sequence(b, row, lane);
-    if (seq < 0 || h >= a.heads) return;
-    const Seq sq = sequence(c, b, seq);
-    int nchunk = (sq.total + pl.chunk - 1) / pl.chunk;
-    nchunk = nchunk > pl.chunks ? pl.chunks : nchunk;
-    if (nchunk <= 1 || row - sq.row0 >= b.max_nodes) return;
+    if (h >= a.heads) return;
     const int64_t prow = part_rows(b.rows, a.heads), at = (int64_t)row * a.heads + h;
     const float* const pout = (const float*)a.work + at * D;
     const float2* const pml = (const float2*)(a.work + (int64_t)pl.chunks * prow * D * 4) + at;
     const int part = lane / PER, d = (lane % PER) * 4;
+    const bool early = AHEAD && pl.chunks <= EARLY * PARTS;
+    f32x4 pre[AHEAD ? EARLY : 1];
+    float2 first = make_float2(-INFINITY, 0.f);
+    if constexpr (AHEAD) if (early) {
+        if (lane < pl.chunks) first = pml[lane * prow];
+#pragma unroll
+        for (int i = 0; i < EARLY; ++i) {
+            const int k = i * PARTS + part;
+            pre[i] = f32x4{0, 0, 0, 0};
+            if (k < pl.chunks) pre[i] = *(const f32x4*)(pout + (int64_t)k * prow * D + d);
+        }
+    }
+    const int seq = row_sequence(b, row, lane);
+    if (seq < 0) return;
+    const Seq sq = sequence(c, b, seq);
+    int nchunk = (sq.total + pl.chunk - 1) / pl.chunk;
+    nchunk = nchunk > pl.chunks ? pl.chunks : nchunk;
+    if (nchunk <= 1 || row - sq.row0 >= b.max_nodes) return;
     float M = -INFINITY, l = 0.f;
     f32x4 y = {0, 0, 0, 0};
     for (int k0 = 0; k0 < nchunk; k0 += 64) {
         float2 x = make_float2(-INFINITY, 0.f);
-        if (k0 + lane < nchunk) x = pml[(k0 + lane) * prow];
+        if (k0 + lane < nchunk) x = early ? first : pml[(k0 + lane) * prow];
         float top = x.x;
 #pragma unroll
         for (int t = 32; t; t >>= 1) top = fmaxf(top, __shfl_xor(top, t, 64));
         const float Mn = fmaxf(M, top);
         if (Mn == -INFINITY) continue;   // nothing seen so far
         const float f = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x.x - Mn);
-        float ls = x.y * f;
-        if (f == 0.f) ls = 0.f;
+        float ls = f == 0.f ? 0.f : x.y * f;
 #pragma unroll
         for (int t = 32; t; t >>= 1) ls += __shfl_xor(ls, t, 64);
         const float keep = M == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(M - Mn);
@@ -656,13 +679,24 @@ __global__ __launch_bounds__(256) void k_join_chunks(KvCache c, KvBatch b, AttnA
         y *= keep;
         M = Mn;
         const int n = nchunk - k0 < 64 ? nchunk - k0 : 64;
+        // every lane takes every turn: the weights are lane reads, 0 where a chunk holds nothing for this row, whatever
+        // its memory
+        if (AHEAD && early) {
+#pragma unroll
+            for (int i = 0; i < (AHEAD ? EARLY : 1); ++i) {
+                const int k = i * PARTS + part;
+                const float w = __shfl(f, k & 63, 64);
+                if (k < n && w != 0.f) y += pre[i] * w;
+            }
+        } else {
 #pragma unroll 8
-        for (int kb = 0; kb < n; kb += PARTS) {   // every lane takes every turn: the weights are lane reads
-            const int k = kb + part;
-            const float w = __shfl(f, k & 63, 64);   // 0 where the chunk holds nothing for this row, whatever its memory
-            f32x4 v = {0, 0, 0, 0};
-            if (k < n) v = *(const f32x4*)(pout + (int64_t)(k0 + k) * prow * D + d);
-            if (k < n && w != 0.f) y += v * w;
+            for (int kb = 0; kb < n; kb += PARTS) {
+                const int k = kb + part;
+                const float w = __shfl(f, k & 63, 64);
+                f32x4 v = {0, 0, 0, 0};
+                if (k < n) v = *(const f32x4*)(pout + (int64_t)(k0 + k) * prow * D + d);
+                if (k < n && w != 0.f) y += v * w;
+            }
         }
     }
 #pragma unroll
@@ -692,7 +726,9 @@ hipError_t launch_dim(const KvCache& c, const KvBatch& b, const AttnArgs& a, con
     else launch_tiles<T, D, 32, 4, 1, NS, O>(c, b, a, pl, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || pl.chunks == 1) return e;
-    hipLaunchKernelGGL((k_join_chunks<D, O>), dim3(b.rows, (a.heads + 3) / 4), dim3(256), 0, s, c, b, a, pl);
+    const dim3 grid(b.rows, (a.heads + 3) / 4);
+    if ((int64_t)b.rows * a.heads <= 2048) hipLaunchKernelGGL((k_join_chunks<D, O, true>), grid, dim3(256), 0, s, c, b, a, pl);
+    else hipLaunchKernelGGL((k_join_chunks<D, O, false>), grid, dim3(256), 0, s, c, b, a, pl);
     return hipGetLastError();
 }
 
