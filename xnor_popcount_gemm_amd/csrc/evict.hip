@@ -6,14 +6,14 @@
 // found 8 bits at a time from the top, by a histogram of the tokens that share
 // the bits found so far; each of its 256 counters has 32 copies, one per LDS
 // bank, because scores cluster (a handful of exponents) and equal addresses of
-// one LDS add run one after the other.  Positions and keys are read once and
-// stay in registers (up to 32 per thread; longer sequences are read again at
-// each pass).  Ties go to the lowest slots, and the free slots below the new
+// one LDS add run one after the other.  Keys are made once and stay in
+// registers (up to 32 per thread; in LDS instead, 32000 slots took 58 us against
+// 51); those of longer sequences are made again at each pass.  Ties go to the lowest slots, and the free slots below the new
 // length are paired in order with the kept tokens above it: a wave owns a run
 // of slots, so three joins of the waves' counts give every rank.
 //
 // Sources are all at or above the new length and destinations all below it, so
-// a second kernel moves K and V rows in any order.  It is bound by memory
+// a second kernel moves K and V rows (and positions and scores) in any order.  It is bound by memory
 // (4.1 TB/s of reads and writes at 117 MB, a plain copy reaches 5.1); the first
 // by its passes: few workgroups, one per head.
 #include <math.h>
@@ -52,17 +52,18 @@ struct EvictLds {
     int part[6][EV / 64];
 };
 
-// The highest of all threads' values.
-__device__ __forceinline__ void block_max(int& last, EvictLds& lds) {
+// The highest of all threads' values.  part: EV / 64 words of its own.
+__device__ __forceinline__ void block_max(int& last, int* part) {
 #pragma unroll
     for (int m = 32; m; m >>= 1) { const int o = __shfl_xor(last, m, 64); last = o > last ? o : last; }
-    if ((threadIdx.x & 63) == 0) lds.part[1][threadIdx.x >> 6] = last;
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = last;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < EV / 64; ++i) last = lds.part[1][i] > last ? lds.part[1][i] : last;
+    for (int i = 0; i < EV / 64; ++i) last = part[i] > last ? part[i] : last;
 }
 
-// KPT: slots per thread that stay in registers; 0: any number, read again.
+// KPT: keys per thread that stay in registers; 0: any number, made again.
+constexpr int BATCH = 16;
 template <int KPT>
 __device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& a, const Seq& sq, int seq, int kh, EvictLds& lds) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -74,8 +75,13 @@ __device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& 
     auto valid_at = [&](int s) {
         return s < sq.ctx || (s < sq.total && (!a.accept || packed_bit(a.accept + seq * a.ld_accept, a.ld_accept, s - sq.ctx)));
     };
-    constexpr int N = KPT ? KPT : 1;
+    constexpr int N = KPT > 0 ? KPT : 1;
     const int mine = (wave + 1) * steps * 64 < sq.total ? (wave + 1) * steps * 64 : sq.total;   // end of the wave's slots
+    auto valid_in_run = [&](int s) {
+        bool v = s < mine;
+        if (__any(v && s >= sq.ctx)) v = v && valid_at(s);
+        return v;
+    };
     uint32_t key[N], valid = 0;   // valid: bit i for slot first + 64 i
     int n = 0, last = INT32_MIN;
     if constexpr (KPT > 0) {
@@ -88,25 +94,31 @@ __device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& 
         }
 #pragma unroll
         for (int i = 0; i < KPT; ++i) {
-            const int s = first + 64 * i;
-            bool v = s < mine;
-            if (__any(v && s >= sq.ctx)) v = v && valid_at(s);
+            const bool v = valid_in_run(first + 64 * i);
             valid |= (uint32_t)v << i;
             n += __popcll(__ballot(v));
             last = v && p[i] > last ? p[i] : last;
         }
-        block_max(last, lds);
+        block_max(last, lds.part[1]);
         const int64_t since = (int64_t)last - a.recent;
 #pragma unroll
         for (int i = 0; i < KPT; ++i) key[i] = p[i] > since ? 0xFFFFFFFFu : score_key(__uint_as_float(key[i]));
     } else {
-        for (int i = 0; i < steps; ++i) {
-            const int s = first + 64 * i;
-            const bool v = valid_at(s);
-            n += __popcll(__ballot(v));
-            if (v) last = pos[s] > last ? pos[s] : last;
+        for (int i0 = 0; i0 < steps; i0 += BATCH) {   // so many loads at a time
+            int32_t p[BATCH];
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const int s = first + 64 * (i0 + j);
+                p[j] = pos[s < mine ? s : 0];
+            }
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const bool v = valid_in_run(first + 64 * (i0 + j));
+                n += __popcll(__ballot(v));
+                last = v && p[j] > last ? p[j] : last;
+            }
         }
-        block_max(last, lds);
+        block_max(last, lds.part[1]);
     }
     int all;
     before_wave(n, lds.part[0], all);
@@ -193,7 +205,7 @@ __device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& 
         int tie = tied;
         each([&](int i, int s, bool v, uint32_t k) {
             const bool st = stays(v, k, tie);
-            if (KPT) kept |= (uint32_t)st << i;
+            if (KPT > 0) kept |= (uint32_t)st << i;
             holes += __popcll(__ballot(s < low && !st));
             movers += __popcll(__ballot(s >= keep && st));
         });
@@ -205,7 +217,7 @@ __device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& 
     {
         int tie = tied, h = hole0, m = mover0;
         each([&](int i, int s, bool v, uint32_t k) {
-            const bool st = KPT ? (kept >> i & 1u) != 0 : stays(v, k, tie);
+            const bool st = KPT > 0 ? (kept >> (i & 31) & 1u) != 0 : stays(v, k, tie);
             const bool hole = s < low && !st, mover = s >= keep && st;
             const uint64_t hm = __ballot(hole), mm = __ballot(mover);
             if (hole) to[h + __popcll(hm & below)] = s;
@@ -214,18 +226,11 @@ __device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& 
             m += __popcll(mm);
             if (s < keep && st && a.pos_out != a.pos_in) a.pos_out[at + s] = pos[s];
             if (s < keep && st && a.score_out != a.score_in) a.score_out[at + s] = score[s];
+            if (s >= keep && s < mine && !st) {   // freed; what moves is cleared once it has been read
+                a.pos_out[at + s] = -1;
+                a.score_out[at + s] = 0.f;
+            }
         });
-    }
-    __syncthreads();
-    for (int i = tid; i < all; i += EV) {
-        const int f = from[i], t = to[i];
-        a.pos_out[at + t] = pos[f];
-        a.score_out[at + t] = score[f];
-    }
-    __syncthreads();
-    for (int s = keep + tid; s < sq.total; s += EV) {
-        a.pos_out[at + s] = -1;
-        a.score_out[at + s] = 0.f;
     }
     if (tid == 0) { work[0] = all; work[1] = keep; }
 }
@@ -244,17 +249,27 @@ __global__ __launch_bounds__(256) void k_evict_move(KvCache c, EvictArgs a) {
     const int32_t* work = a.work + ((int64_t)seq * c.kv_heads + kh) * evict_work_words(c.capacity);
     const int32_t* from = work + 16;
     const int32_t* to = from + evict_work_words(c.capacity) / 2 - 8;
+    const int64_t at = ((int64_t)seq * c.kv_heads + kh) * a.ld_slots;
     const int64_t n = (int64_t)work[0] * units;
     if (blockIdx.x == 0 && kh == 0 && threadIdx.x == 0) a.ctx_out[seq] = work[1];
     for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
         const int m = (int)(i / units), u = (int)(i % units);
+        const int f = from[m], t = to[m];
+        if (u == 0) {   // its position and score, and the slot it leaves
+            const int32_t p = a.pos_in[at + f];
+            const float x = a.score_in[at + f];
+            a.pos_out[at + t] = p;
+            a.score_out[at + t] = x;
+            a.pos_out[at + f] = -1;
+            a.score_out[at + f] = 0.f;
+        }
         uint32_t sp, dp;
-        const int32_t spg = slot_page(c, seq, from[m], sp), dpg = slot_page(c, seq, to[m], dp);
+        const int32_t spg = slot_page(c, seq, f, sp), dpg = slot_page(c, seq, t, dp);
         if (spg < 0 || dpg < 0) continue;
-        *(u32x4*)(c.K + dpg * c.k_page + dp * c.k_slot + kh * c.k_head + u * 16) =
-            *(const u32x4*)(c.K + spg * c.k_page + sp * c.k_slot + kh * c.k_head + u * 16);
-        *(u32x4*)(c.V + dpg * c.v_page + dp * c.v_slot + kh * c.v_head + u * 16) =
-            *(const u32x4*)(c.V + spg * c.v_page + sp * c.v_slot + kh * c.v_head + u * 16);
+        const u32x4 k = *(const u32x4*)(c.K + spg * c.k_page + sp * c.k_slot + kh * c.k_head + u * 16);
+        const u32x4 v = *(const u32x4*)(c.V + spg * c.v_page + sp * c.v_slot + kh * c.v_head + u * 16);
+        *(u32x4*)(c.K + dpg * c.k_page + dp * c.k_slot + kh * c.k_head + u * 16) = k;
+        *(u32x4*)(c.V + dpg * c.v_page + dp * c.v_slot + kh * c.v_head + u * 16) = v;
     }
 }
 
