@@ -7,7 +7,8 @@ namespace {
 // Rows per (sequence, key head) decide the workgroup: up to 16 or 32 rows one
 // row tile whose waves share out the slots, above that row tiles of 64 or 128
 // whose waves share the fetched K and V.
-AttnPlan make_plan(int32_t dim, int32_t kv_heads, const KvBatch& b, int32_t heads) {
+AttnPlan make_plan(const KvCache& c, const KvBatch& b, int32_t heads) {
+    const int32_t dim = c.dim, kv_heads = c.kv_heads;
     AttnPlan p;
     const int64_t rows = (int64_t)b.max_nodes * (heads / kv_heads);
     const int32_t kw = dim == 256 ? 2 : 4;
@@ -18,7 +19,7 @@ AttnPlan make_plan(int32_t dim, int32_t kv_heads, const KvBatch& b, int32_t head
     const int64_t tile = p.R * p.RW;
     const int64_t tiles = (rows + tile - 1) / tile;
     p.row_tiles = (int32_t)tiles;
-    const int64_t slots = (int64_t)b.max_ctx + b.max_nodes;
+    const int64_t bound = (int64_t)b.max_ctx + b.max_nodes, slots = bound < c.capacity ? bound : c.capacity;
     const int64_t unit = p.RW == 4 ? 256 : 128;      // slots of whole steps, whatever the variant
     // About the 512 workgroups that are resident at once (256 compute units, 2 each): twice as many cost the
     // compute-bound cases 7 to 17% (the partial results of more chunks are written and read again).  Streaming
@@ -40,15 +41,15 @@ AttnPlan make_plan(int32_t dim, int32_t kv_heads, const KvBatch& b, int32_t head
 
 }  // namespace
 
-int64_t tree_attention_work(int32_t dim, int32_t kv_heads, const KvBatch& b, int32_t heads) {
-    const AttnPlan p = make_plan(dim, kv_heads, b, heads);
+int64_t tree_attention_work(const KvCache& c, const KvBatch& b, int32_t heads) {
+    const AttnPlan p = make_plan(c, b, heads);
     if (p.groups < 0) return -1;
-    return p.chunks == 1 ? 0 : (int64_t)p.chunks * b.rows * heads * (dim * 4 + 8);
+    return p.chunks == 1 ? 0 : (int64_t)p.chunks * b.rows * heads * (c.dim * 4 + 8);
 }
 
 hipError_t launch_tree_attention(const KvCache& c, const KvBatch& b, const AttnArgs& a, int32_t dtype, int32_t out_dtype,
                                  hipStream_t s) {
-    const AttnPlan p = make_plan(c.dim, c.kv_heads, b, a.heads);
+    const AttnPlan p = make_plan(c, b, a.heads);
     if (dtype == KV_BF16) return out_dtype == KV_F32 ? attn_bf16_f32(c, b, a, p, s) : attn_bf16(c, b, a, p, s);
     return out_dtype == KV_F32 ? attn_f16_f32(c, b, a, p, s) : attn_f16(c, b, a, p, s);
 }

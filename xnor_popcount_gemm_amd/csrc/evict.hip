@@ -8,14 +8,16 @@
 // bank, because scores cluster (a handful of exponents) and equal addresses of
 // one LDS add run one after the other.  Keys are made once and stay in
 // registers (up to 32 per thread; in LDS instead, 32000 slots took 58 us against
-// 51); those of longer sequences are made again at each pass.  Ties go to the lowest slots, and the free slots below the new
-// length are paired in order with the kept tokens above it: a wave owns a run
-// of slots, so three joins of the waves' counts give every rank.
+// 51); those of longer sequences are made again at each pass.  Ties go to the
+// lowest slots, and the free slots below the new length are paired in order
+// with the kept tokens above it: a wave owns a run of slots, so three joins of
+// the waves' counts give every rank.
 //
 // Sources are all at or above the new length and destinations all below it, so
-// a second kernel moves K and V rows (and positions and scores) in any order.  It is bound by memory
-// (4.1 TB/s of reads and writes at 117 MB, a plain copy reaches 5.1); the first
-// by its passes: few workgroups, one per head.
+// a second kernel moves K and V rows (and positions and scores) in any order.
+// It is bound by memory: 117 MB of reads and writes in 30 us, 3.9 TB/s, where a
+// plain copy reaches 5.1.  The first kernel is bound by its passes in one
+// workgroup per head: 13 us at 2048 slots, 51 at 32000.
 #include <math.h>
 
 #include "bnn_device.hpp"
@@ -276,7 +278,7 @@ __global__ __launch_bounds__(256) void k_evict_move(KvCache c, EvictArgs a) {
 }  // namespace
 
 hipError_t launch_cache_evict(const KvCache& c, const KvBatch& b, const EvictArgs& a, hipStream_t s) {
-    const int64_t rows = (int64_t)b.max_ctx + b.max_nodes;
+    const int64_t bound = (int64_t)b.max_ctx + b.max_nodes, rows = bound < c.capacity ? bound : c.capacity;
     const dim3 heads(c.kv_heads, b.B);
     if (rows <= 4 * EV) hipLaunchKernelGGL((k_evict_select<4>), heads, dim3(EV), 0, s, c, b, a);
     else if (rows <= 8 * EV) hipLaunchKernelGGL((k_evict_select<8>), heads, dim3(EV), 0, s, c, b, a);

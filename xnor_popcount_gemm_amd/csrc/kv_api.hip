@@ -201,7 +201,7 @@ int64_t bnn_tree_attention_workspace(const bnn_kv_cache* cache, const bnn_kv_bat
     KvBatch b;
     if (make_batch(batch, b, true) != BNN_OK || make_cache(cache, batch->B, c, true) != BNN_OK) return -1;
     if (check_heads(heads, c.kv_heads) != BNN_OK) return -1;
-    return bnn::tree_attention_work(c.dim, c.kv_heads, b, (int32_t)heads);
+    return bnn::tree_attention_work(c, b, (int32_t)heads);
 }
 
 bnn_status bnn_tree_attention(const bnn_kv_cache* cache, const bnn_kv_batch* batch, const bnn_attn_args* a, bnn_stream_t stream) {
@@ -221,7 +221,7 @@ bnn_status bnn_tree_attention(const bnn_kv_cache* cache, const bnn_kv_batch* bat
         if (a->ld_lse < a->heads) return BNN_ERR_LD;
         if (misaligned(a->lse, 4)) return BNN_ERR_ALIGN;
     }
-    const int64_t need = bnn::tree_attention_work(c.dim, c.kv_heads, b, (int32_t)a->heads);
+    const int64_t need = bnn::tree_attention_work(c, b, (int32_t)a->heads);
     if (need < 0) return BNN_ERR_SHAPE;   // more workgroups than a launch takes
     BNN_TRY(check_work(a->workspace, a->workspace_bytes, need));
     if (b.rows == 0 || b.B == 0 || b.max_nodes == 0) return BNN_OK;

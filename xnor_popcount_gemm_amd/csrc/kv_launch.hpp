@@ -34,7 +34,8 @@ struct AttnArgs {
     char* work;
 };
 
-int64_t tree_attention_work(int32_t dim, int32_t kv_heads, const KvBatch& b, int32_t heads);
+// Workspace bytes; -1 where a launch would not take the grid.
+int64_t tree_attention_work(const KvCache& c, const KvBatch& b, int32_t heads);
 hipError_t launch_tree_attention(const KvCache& c, const KvBatch& b, const AttnArgs& a, int32_t dtype, int32_t out_dtype,
                                  hipStream_t s);
 

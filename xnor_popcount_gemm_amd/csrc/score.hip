@@ -17,7 +17,8 @@
 // The grid is what fits the chip at once, and each wave takes an equal run of
 // all tiles in the order sequence, key head, tile: sequences of any lengths
 // are balanced, and a wave's start (page lookup, list of rows, Q) is paid once
-// or twice.
+// or twice.  16 sequences of 9000 to 16000 slots, 20 rows: 76 us, 4.9 TB/s (the
+// same loads alone, nothing computed: 6.2).
 #include <math.h>
 
 #include "bnn_device.hpp"
@@ -322,7 +323,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
 template <typename T, int D>
 void launch_one(const KvCache& c, const KvBatch& b, const ScoreArgs& a, hipStream_t s) {
     constexpr int PER_CU = D == 64 ? 4 : D == 96 ? 3 : D == 128 ? 2 : 1;   // by LDS
-    const int64_t slots = (int64_t)b.max_ctx + b.max_nodes;
+    const int64_t bound = (int64_t)b.max_ctx + b.max_nodes, slots = bound < c.capacity ? bound : c.capacity;
     const int64_t tiles = (slots / 32 + 1 + START) * c.kv_heads * b.B;
     int64_t blocks = (tiles + 3) / 4;
     const int64_t most = (int64_t)num_cus() * PER_CU;   // what is resident at once
