@@ -279,6 +279,77 @@ def test_attention_extreme_logits(bnn, T, heads, kv):
     check_attention(case, cache, q, seen, got, lse, 0.09)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.07])
+@pytest.mark.parametrize("T,heads,kv", [(1, 4, 1), (11, 4, 2), (50, 8, 2)])
+def test_attention_zero_and_negative_scale(bnn, scale, T, heads, kv):
+    banner(f"tree_attention scale {scale} T={T}")
+    case = (BF, torch.float32, heads, kv, 64, [210], [T], 16, "token", True, True)
+    rng, cache, q, mask, seen = make_attention(case, seed=31)
+    got, lse = bnn.tree_attention(q.cuda(), cache.device(bnn), cuda_i32([0, T]), cuda_i32([210]), max_nodes=T, max_ctx=210, mask=mask.cuda(), scale=scale,
+                                  out_dtype=torch.float32)
+    out, want = got.double().cpu().numpy(), lse.double().cpu().numpy()
+    k, v = (cache.get(w, 0, np.arange(210 + T)) for w in "KV")
+    for i in range(T):
+        y, l, A, S = ref.attention(q[i].double().numpy(), k, v, ref.sees(210, T, i, np.isin(np.arange(T), list(seen[i]))), scale)
+        ds = (64 + 10) * ref.E32 * np.abs(S)
+        assert (np.abs(want[i] - l) <= ds + (210 + T + 8) * ref.E32 + 8 * ref.E32 * np.abs(l)).all()
+        assert (np.abs(out[i] - y) <= (2.0 ** -22 + 2.0 ** -24 + 2 * ds + 2 * (210 + T) * ref.E32)[:, None] * A + 2.0 ** -26).all()
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_attention_missing_page(bnn, T):
+    """A table entry that names no page reads as rows of zeros."""
+    banner(f"tree_attention missing page T={T}")
+    case = (FP, torch.float32, 8, 2, 128, [200], [T], 16, "token", True, True)
+    rng, cache, q, mask, seen = make_attention(case, seed=32)
+    for w in "KV":
+        cache.put(w, 0, np.arange(48, 64), np.zeros((16, 2, 128)))
+    args = dict(max_nodes=T, max_ctx=200, mask=mask.cuda(), out_dtype=torch.float32)
+    want, l0 = bnn.tree_attention(q.cuda(), cache.device(bnn), cuda_i32([0, T]), cuda_i32([200]), **args)
+    for bad in (-1, 1 << 30):
+        cache.table[0, 3] = bad
+        dc = cache.device(bnn, score=torch.zeros((1, 2, cache.slots), device="cuda"))
+        got, l1 = bnn.tree_attention(q.cuda(), dc, cuda_i32([0, T]), cuda_i32([200]), **args)
+        assert torch.equal(got, want) and torch.equal(l0, l1)
+        assert bnn.cache_score_add(q.cuda(), l1, dc, cuda_i32([0, T]), cuda_i32([200]), max_nodes=T, max_ctx=200, mask=mask.cuda()).isfinite().all()
+
+
+def test_many_sequences(bnn):
+    """130 short sequences, some without committed and some without new tokens:
+    every call's way from a row or a share of the work to its sequence."""
+    banner("130 sequences")
+    rng = np.random.default_rng(33)
+    B, heads, kv, dim = 130, 4, 2, 64
+    ctx, nodes = rng.integers(0, 70, B), rng.integers(0, 4, B)
+    ctx[[0, 64, 129]], nodes[[0, 63, 65, 128]] = 0, 0
+    case = (BF, torch.float32, heads, kv, dim, ctx.tolist(), nodes.tolist(), 8, "token", False, True)
+    _, cache, q, _, _ = make_attention(case, seed=34)
+    rows = int(nodes.sum())
+    score = torch.zeros((B, kv, cache.slots), device="cuda")
+    pos = torch.full((B, kv, cache.slots), -1, dtype=torch.int32, device="cuda")
+    dc = cache.device(bnn, pos, score)
+    indptr, dctx = cuda_i32(np.concatenate(([0], np.cumsum(nodes)))), cuda_i32(ctx)
+    k, v = torch.from_numpy(rng.standard_normal((2, rows, kv, dim))).float()
+    qr = bnn.qk_norm_rope(q.float().cuda(), k.cuda(), v.cuda(), dc, indptr, dctx, cuda_i32(range(rows)), None)
+    assert torch.equal(qr.cpu(), q)
+    starts = np.concatenate(([0], np.cumsum(nodes)))
+    for b in range(B):
+        s = ctx[b] + np.arange(nodes[b])
+        rows_b = slice(starts[b], starts[b + 1])
+        assert torch.equal(pos.cpu()[b][:, s], torch.arange(rows, dtype=torch.int32)[rows_b].expand(kv, -1))
+        cache.put("K", b, s, k[rows_b])
+        cache.put("V", b, s, v[rows_b])
+    args = dict(max_nodes=3, max_ctx=70)
+    out, lse = bnn.tree_attention(qr, dc, indptr, dctx, out_dtype=torch.float32, **args)
+    torch.cuda.synchronize()
+    check_attention(case, cache, q, None, out, lse, dim ** -0.5)
+    # the weights of a row add up to the heads of its group, so the sums count the rows
+    total = bnn.cache_score_add(qr, lse, dc, indptr, dctx, **args).double().sum(-1).cpu().numpy()
+    assert np.allclose(total, nodes[:, None] * (heads // kv) * np.ones((1, kv)), rtol=2e-5, atol=0)
+    got = bnn.cache_evict(dc, indptr, dctx, budget=50, recent=0, **args)
+    assert np.array_equal(got.cpu().numpy(), np.minimum(ctx + nodes, 50))
+
+
 def test_attention_far_pages(bnn):
     """Rows that lie past 2^32 bytes of the cache's start."""
     banner("tree_attention far pages")
