@@ -638,8 +638,7 @@ _pack_batch, _pack_rope, _pack_attn, _pack_score, _pack_evict = (
     _layout(t).pack for t in (_KvBatch, _RopeArgs, _AttnArgs, _ScoreArgs, _EvictArgs))
 
 
-def _raw_stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 BF16, F16, F32 = 1, 2, 3
@@ -669,6 +668,7 @@ class KVCache:
         pages, page, heads, dim = k.shape
         self.k, self.v, self.table, self.pos, self.score = k, v, table, pos, score
         self.device, self.dtype = k.device, k.dtype
+        self._index = k.device.index
         self.kv_heads, self.dim, self.page_size = heads, dim, page
         c = self._c = _KvCache()
         c.K, c.k_page, c.k_slot, c.k_head = k.data_ptr(), k.stride(0), k.stride(1), k.stride(2)
@@ -782,7 +782,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCac
     dim = cache.dim
     kv = cache.kv_heads
     if q_out is None:
-        q_out = torch.empty((rows, heads, dim), dtype=cache.dtype, device=q.device)
+        q_out = q.new_empty((rows, heads, dim), dtype=cache.dtype)
     table, max_pos, rot = 0, 0, 0
     if turns is not None:
         if turns.dim() != 2:
@@ -802,7 +802,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCac
                    _flat(positions, torch.int32, "positions", rows), table, max_pos, rot, 1 if interleaved else 0,
                    0 if q_weight is None else _flat(q_weight, torch.float32, "q_weight", dim),
                    0 if k_weight is None else _flat(k_weight, torch.float32, "k_weight", dim), eps, pos, score, slots)
-    _check((_lib or lib()).bnn_qk_norm_rope(cache._ref, _batch(cache, indptr, ctx, rows, rows, 0), a, _raw_stream(q.device)),
+    _check((_lib or lib()).bnn_qk_norm_rope(cache._ref, _batch(cache, indptr, ctx, rows, rows, 0), a, _raw_stream(cache._index)),
            "bnn_qk_norm_rope")
     return q_out
 
@@ -831,9 +831,9 @@ def tree_attention(q: torch.Tensor, cache: KVCache, indptr: torch.Tensor, ctx: t
     rows, heads, dim = q.shape
     b = _batch(cache, indptr, ctx, rows, max_nodes, max_ctx)
     if out is None:
-        out = torch.empty((rows, heads, dim), dtype=out_dtype or cache.dtype, device=q.device)
+        out = q.new_empty((rows, heads, dim), dtype=out_dtype or cache.dtype)
     if lse is None:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((rows, heads), dtype=torch.float32)
     kind = out.dtype
     if kind is not torch.float32 and kind is not cache.dtype:
         raise TypeError(f"out must be torch.float32 or {cache.dtype} (got {kind})")
@@ -844,7 +844,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, indptr: torch.Tensor, ctx: t
                    dim ** -0.5 if scale is None else scale, *_token_rows(out, kind, "out", rows, heads, dim),
                    F32 if kind is torch.float32 else _KV_TYPES[kind], *_row_floats(lse, "lse", rows, heads),
                    workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _check(L.bnn_tree_attention(cache._ref, b, a, _raw_stream(q.device)), "bnn_tree_attention")
+    _check(L.bnn_tree_attention(cache._ref, b, a, _raw_stream(cache._index)), "bnn_tree_attention")
     return out, lse
 
 
@@ -866,7 +866,7 @@ def cache_score_add(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, indptr: 
     a = _pack_score(*_token_rows(q, cache.dtype, "q", rows, heads, cache.dim), heads, *_row_floats(lse, "lse", rows, heads),
                     *_bit_rows(mask, "mask", rows), *_bit_rows(accept, "accept", ctx.numel()), dim ** -0.5 if scale is None else scale,
                     cache.score.data_ptr(), score_out.data_ptr(), cache.score.shape[2])
-    _check((_lib or lib()).bnn_cache_score_add(cache._ref, _batch(cache, indptr, ctx, rows, max_nodes, max_ctx), a, _raw_stream(q.device)),
+    _check((_lib or lib()).bnn_cache_score_add(cache._ref, _batch(cache, indptr, ctx, rows, max_nodes, max_ctx), a, _raw_stream(cache._index)),
            "bnn_cache_score_add")
     return score_out
 
@@ -905,6 +905,6 @@ def cache_evict(cache: KVCache, indptr: torch.Tensor, ctx: torch.Tensor, *, budg
     a = _pack_evict(*_bit_rows(accept, "accept", ctx.numel()), budget, recent, cache.pos.data_ptr(), pos_out.data_ptr(),
                     cache.score.data_ptr(), score_out.data_ptr(), slots[2], ctx_out.data_ptr(), workspace.data_ptr(),
                     workspace.numel() * workspace.element_size())
-    _check((_lib or lib()).bnn_cache_evict(cache._ref, _batch(cache, indptr, ctx, 1 << 30, max_nodes, max_ctx), a, _raw_stream(cache.device)),
+    _check((_lib or lib()).bnn_cache_evict(cache._ref, _batch(cache, indptr, ctx, 1 << 30, max_nodes, max_ctx), a, _raw_stream(cache._index)),
            "bnn_cache_evict")
     return ctx_out

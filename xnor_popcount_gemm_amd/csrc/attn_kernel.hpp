@@ -695,7 +695,6 @@ __global__ __launch_bounds__(256) void k_join_chunks(KvCache c, KvBatch b, AttnA
                 if (k < n && w != 0.f) y += pre[i] * w;
             }
         } else {
-#pragma unroll 8
             for (int kb = 0; kb < n; kb += PARTS) {
                 const int k = kb + part;
                 const float w = __shfl(f, k & 63, 64);
