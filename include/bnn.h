@@ -570,8 +570,11 @@ typedef struct bnn_attn_args {
  * with products and sums in fp32.  A row that sees nothing gives 0 and
  * lse = -inf.  Values of unseen tokens do not matter, NaN and infinities
  * included.  With a 16-bit out the weights are rounded to that type for the
- * product with V; with fp32 out they keep 22 bits or more.  The workspace's
- * contents need not be kept or cleared between calls. */
+ * product with V; with fp32 out they keep 22 bits or more.  A weight of a
+ * float16 cache may also be off by 2^-30 of the largest weight among the 64
+ * slots around it (slots 64 i .. 64 i + 63), which is what remains of weights
+ * 2^16 times smaller than a neighbour's and less.  The workspace's contents
+ * need not be kept or cleared between calls. */
 bnn_status bnn_tree_attention(const bnn_kv_cache* cache, const bnn_kv_batch* batch,
                               const bnn_attn_args* args, bnn_stream_t stream);
 

@@ -16,7 +16,12 @@
 // Running maximum.  Weights are taken relative to a reference that is only
 // raised when a score passes it by more than 2^8 (in the base-2 logarithm):
 // the result is the same, and the accumulators are rescaled a few times
-// instead of at every step.
+// instead of at every step.  bfloat16 weights have fp32's exponents, so that is
+// all; float16 ones end at 2^-24, and slots far below one that dominates the
+// row (whose V may be near 0) would be lost.  There the reference follows each
+// step's maximum both ways, so that the step's largest weight lies in
+// 2^5 .. 2^15 (2^12 where it is moved, at most 2^48 below its peak): a weight is
+// then off by its rounding or by 2^-30 of the largest of its 32 or 64 slots.
 //
 // Tiles.  K and V rows go from global memory straight to LDS (16 bytes per
 // lane); the next step's rows are in flight while one is worked on, in a
@@ -149,6 +154,10 @@ struct Attn {
         const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tp)(base + o + VSTEP));
         return __builtin_bit_cast(vec8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     }
+
+    // base-2 logarithms of a float16 step's largest weight: bounds, where it is put, and how far the reference may sink
+    static constexpr bool NARROW = std::is_same<T, F16>::value;
+    static constexpr float HIGH = NARROW ? 15.f : 8.f, LOW = 5.f, AIM = 12.f, DEEP = 48.f;
 
     static constexpr int PW = (OB * (int)sizeof(acc) / 4 + 31) / 32;   // words of a bit per accumulator
 
@@ -291,6 +300,7 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
 #pragma unroll
     for (int i = 0; i < A::OB; ++i) o[i] = acc{};
     float m = -INFINITY, l = 0.f;   // reference (base-2 logarithm) and this lane's share of the sum
+    float peak = -INFINITY;         // the highest reference so far
     // which of this lane's dimensions saw +inf / -inf: bit 4 i + e of dimension e of its piece i of 4
     uint32_t plus[A::PW], minus[A::PW];
 #pragma unroll
@@ -366,10 +376,17 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
 #pragma unroll
             for (int i = 0; i < A::NSC; ++i) mx = fmaxf(mx, sc[sub][i]);
         mx = row_max<R>(mx) * c2;
-        if (__any(mx > m + 8.f)) {
-            const float mn = fmaxf(m, mx);
+        bool move = mx > m + A::HIGH;
+        float mn = fmaxf(m, mx);
+        if constexpr (A::NARROW) {
+            const float want = fmaxf(mx - A::AIM, peak - A::DEEP);
+            move = move || (mx > -INFINITY && want < m - (A::AIM - A::LOW));
+            mn = move ? want : m;
+        }
+        if (__any(move)) {
             const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
             m = mn;
+            if (A::NARROW) peak = fmaxf(peak, m);
             l *= f;
 #pragma unroll
             for (int i = 0; i < A::OB; ++i) o[i] *= f;
