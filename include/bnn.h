@@ -620,8 +620,8 @@ typedef struct bnn_evict_args {
 /* Drops the new tokens that were not accepted, then cuts each sequence to
  * keep = min(budget, what is left) tokens, for each key head its own choice:
  * first the tokens whose position exceeds the highest one left minus recent,
- * then by score, the highest first; equal scores by slot, the lowest first; a
- * NaN score counts as -inf.  In place: tokens kept in slots below keep stay;
+ * then all others; among either by score, the highest first; equal scores by
+ * slot, the lowest first; a NaN score counts as -inf.  In place: tokens kept in slots below keep stay;
  * the others, in order, fill the slots below keep that became free, in
  * order.  K, V, pos and score move alike; the freed slots up to the old
  * length get pos -1 and score 0, and ctx_out[b] = keep.  Calling it again

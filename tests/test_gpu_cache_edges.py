@@ -1,5 +1,6 @@
 """GPU checks of the calls over the paged key/value cache at the edges of their
-definitions: weights far below one that dominates its row.
+definitions: weights far below one that dominates its row, evictions where the
+recent tokens alone exceed the budget.
 
 Bounds as in test_gpu_cache.py: u is half an ulp of a type as a ratio, products
 and sums in fp32 add (D + 10) 2^-24 sum |q k| scale to a logit and n 2^-24 to a
@@ -74,3 +75,67 @@ def test_attention_one_token_dominates(bnn, T, out, gap):
             bound = own + far + (2 * ds[h] + 2 * (n / 16 + 40) * ref.E32) * A[h]
             err = np.abs(got[0, i, h] - y[h])
             assert (err <= bound).all(), (i, h, float((err / bound).max()), float((err / np.abs(y[h])).max()))
+
+
+# ---- recent tokens that alone exceed the budget
+
+def evict_by_rank(ctx, accepted, budget, recent, pos, score):
+    """One (sequence, head) by the definition: recent tokens first, then by
+    score (NaN as -inf), equal scores by slot.  Returns the source slot of each
+    kept one."""
+    valid = np.concatenate((np.arange(ctx), ctx + np.flatnonzero(accepted))).astype(np.int64)
+    keep = min(len(valid), budget)
+    w = np.where(np.isnan(score[valid]), -np.inf, score[valid].astype(np.float64))
+    late = pos[valid].astype(np.int64) > (int(pos[valid].max()) - recent if len(valid) else 0)
+    stay = np.sort(valid[np.lexsort((valid, -w, ~late))[:keep]])
+    source = np.arange(keep)
+    source[np.setdiff1d(source, stay)] = stay[stay >= keep]
+    return source
+
+
+@pytest.mark.parametrize("inplace", (False, True))
+@pytest.mark.parametrize("case", [
+    # ctx, nodes, budget, recent
+    ([12], [1], 4, 100), ([1500], [3], 700, 2000), ([0, 1, 90, 300], [9, 3, 0, 5], 7, 40), ([3000], [8], 64, 64), ([3000], [8], 64, 65),
+    ([3000], [8], 64, 63), ([7000, 60], [31, 31], 1, 1 << 40), ([14000], [2], 5000, 9000), ([30000], [1], 300, 20000),
+    ([40000, 33000], [1, 64], 2500, 30000), ([500], [4], 0, 300)], ids=range(11))
+def test_evict_more_recent_tokens_than_the_budget(bnn, case, inplace):
+    ctx, nodes, budget, recent = case
+    banner(f"cache_evict recent over the budget {case} inplace={inplace}")
+    rng = np.random.default_rng(51)
+    B, kv, dim = len(ctx), 2, 64
+    cache = ref.Paged(rng, B, max(c + t for c, t in zip(ctx, nodes)) + 2, 16, kv, dim, BF)
+    pos = np.full((B, kv, cache.slots), -3, dtype=np.int32)
+    score = np.full((B, kv, cache.slots), 2.5, dtype=np.float32)
+    accepted = [rng.random(t) < 0.6 for t in nodes]
+    for b in range(B):
+        n = ctx[b] + nodes[b]
+        for w in "KV":
+            cache.put(w, b, np.arange(n), rng.standard_normal((n, kv, dim)))
+        for h in range(kv):
+            pos[b, h, :n] = rng.permutation(n)
+            x = rng.standard_normal(n).astype(np.float32) ** 2
+            x[rng.random(n) < 0.3] = rng.choice(np.array([0.0, -0.0, 1.0, np.inf, -np.inf, np.nan], dtype=np.float32))
+            score[b, h, :n] = x
+    before = cache.K.clone(), cache.V.clone()
+    dpos, dscore, dctx = torch.from_numpy(pos.copy()).cuda(), torch.from_numpy(score.copy()).cuda(), cuda_i32(ctx)
+    dc = cache.device(bnn, dpos, dscore)
+    kw = {} if inplace else dict(pos_out=torch.full_like(dpos, -9), score_out=torch.full_like(dscore, -9.0), ctx_out=torch.full_like(dctx, -9))
+    got = bnn.cache_evict(dc, cuda_i32(np.concatenate(([0], np.cumsum(nodes)))), dctx, budget=budget, recent=recent, max_nodes=max(nodes),
+                          max_ctx=max(ctx), accept=ref.packed([np.flatnonzero(a) for a in accepted], 2).cuda(), **kw)
+    torch.cuda.synchronize()
+    pos2, score2 = (x.cpu().numpy() for x in ((dpos, dscore) if inplace else (kw["pos_out"], kw["score_out"])))
+    wantK, wantV = before[0].clone(), before[1].clone()
+    for b in range(B):
+        n = ctx[b] + nodes[b]
+        for h in range(kv):
+            source = evict_by_rank(ctx[b], accepted[b], budget, recent, pos[b, h, :n], score[b, h, :n])
+            keep = len(source)
+            assert got[b] == keep
+            assert np.array_equal(pos2[b, h, :keep], pos[b, h, source]) and (pos2[b, h, keep:n] == -1).all()
+            assert np.array_equal(score2[b, h, :keep].view(np.int32), score[b, h, source].view(np.int32)) and (score2[b, h, keep:n] == 0).all()
+            if keep:
+                to, come = cache.at(b, np.arange(keep)), cache.at(b, source)
+                wantK[(*to, h)], wantV[(*to, h)] = before[0][(*come, h)], before[1][(*come, h)]
+    same = lambda x, y: torch.equal(x.contiguous().view(torch.int16), y.contiguous().view(torch.int16))
+    assert same(cache.dK.cpu(), wantK) and same(cache.dV.cpu(), wantV)

@@ -9,9 +9,11 @@
 // one LDS add run one after the other.  Keys are made once and stay in
 // registers (up to 32 per thread; in LDS instead, 32000 slots took 58 us against
 // 51); those of longer sequences are made again at each pass.  Ties go to the
-// lowest slots, and the free slots below the new length are paired in order
-// with the kept tokens above it: a wave owns a run of slots, so three joins of
-// the waves' counts give every rank.
+// lowest slots.  Where recent tokens are among those that leave, they alone fill
+// the new length, and the search is made again over them, by their scores.  The
+// free slots below the new length are paired in order with the kept tokens above
+// it: a wave owns a run of slots, so three joins of the waves' counts give every
+// rank.
 //
 // Sources are all at or above the new length and destinations all below it, so
 // a second kernel moves K and V rows (and positions and scores) in any order.
@@ -65,9 +67,12 @@ __device__ __forceinline__ void block_max(int& last, int* part) {
 }
 
 // KPT: keys per thread that stay in registers; 0: any number, made again.
+// Returns false, with nothing written, where KPT > 0 and recent tokens leave:
+// keys of a second search beside the first's would not stay in registers (20 us
+// more at 32000 slots for every call).
 constexpr int BATCH = 16;
 template <int KPT>
-__device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& a, const Seq& sq, int seq, int kh, EvictLds& lds) {
+__device__ __forceinline__ bool evict_select(const KvCache& c, const EvictArgs& a, const Seq& sq, int seq, int kh, EvictLds& lds) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t at = ((int64_t)seq * c.kv_heads + kh) * a.ld_slots;
     const float* const score = a.score_in + at;
@@ -128,7 +133,8 @@ __device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& 
     const int keep = n < a.budget ? n : a.budget;
     const int64_t since = (int64_t)last - a.recent;
     const int low = keep < mine ? keep : mine;   // this wave's slots below the new length end here
-    // f(i, slot, valid, key) for this thread's slots, every thread of a wave alike
+    bool crowded = false;   // recent tokens leave: only they may stay, by score
+    // f(i, slot, may stay, key) for this thread's slots, every thread of a wave alike
     auto each = [&](auto f) {
         if constexpr (KPT > 0) {
 #pragma unroll
@@ -137,8 +143,8 @@ __device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& 
         } else {
             for (int i = 0; i < steps; ++i) {
                 const int s = first + 64 * i;
-                const bool v = valid_at(s);
-                f(i, s, v, !v ? 0u : pos[s] > since ? 0xFFFFFFFFu : score_key(score[s]));
+                const bool v = valid_at(s), recent = v && pos[s] > since;
+                f(i, s, crowded ? recent : v, !v ? 0u : recent && !crowded ? 0xFFFFFFFFu : score_key(score[s]));
             }
         }
     };
@@ -148,7 +154,7 @@ __device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& 
     int ties = keep;
     const bool cut = keep < n && keep > 0;
     if (cut) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
+        for (int shift = 24; shift >= 0;) {
             for (int i = tid; i < 256 * 32; i += EV) lds.hist[i] = 0;
             __syncthreads();
             each([&](int, int, bool v, uint32_t k) {
@@ -183,6 +189,14 @@ __device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& 
             }
             edge |= (uint32_t)__builtin_amdgcn_readlane(digit, hit) << shift;
             ties -= __builtin_amdgcn_readlane(above, hit);
+            shift -= 8;
+            if (shift < 0 && edge == 0xFFFFFFFFu && !crowded && lds.bins[255] > (uint32_t)ties) {
+                if (KPT > 0) return false;
+                crowded = true;
+                shift = 24;
+                edge = 0;
+                ties = keep;
+            }
         }
     }
 
@@ -235,6 +249,7 @@ __device__ __forceinline__ void evict_select(const KvCache& c, const EvictArgs& 
         });
     }
     if (tid == 0) { work[0] = all; work[1] = keep; }
+    return true;
 }
 
 template <int KPT>
@@ -242,8 +257,7 @@ __global__ __launch_bounds__(EV) void k_evict_select(KvCache c, KvBatch b, Evict
     __shared__ EvictLds lds;
     const int kh = blockIdx.x, seq = blockIdx.y;
     const Seq sq = sequence(c, b, seq);
-    if (sq.total <= EV * KPT) evict_select<KPT>(c, a, sq, seq, kh, lds);
-    else evict_select<0>(c, a, sq, seq, kh, lds);
+    if (sq.total > EV * KPT || !evict_select<KPT>(c, a, sq, seq, kh, lds)) evict_select<0>(c, a, sq, seq, kh, lds);
 }
 
 __global__ __launch_bounds__(256) void k_evict_move(KvCache c, EvictArgs a) {
