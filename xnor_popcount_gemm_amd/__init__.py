@@ -654,7 +654,8 @@ class KVCache:
     transposed).  ``table``: int32 [B, pages per sequence], or None where
     sequence b owns page b.  ``pos`` int32 and ``score`` float32
     [B, kv_heads, slots]: the position and the running attention weight of
-    each slot, for the calls that keep or read them.  The tensors are kept
+    each slot, for the calls that keep or read them; with a table a row for
+    each of its sequences, without one their rows bound the sequences.  The tensors are kept
     alive by this object and used in place."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor | None = None, *,
@@ -684,11 +685,14 @@ class KVCache:
         for t, dtype, name in ((pos, torch.int32, "pos"), (score, torch.float32, "score")):
             if t is not None:
                 self._check_slots(_dev(t, dtype, name), name)
+                self.sequences = min(self.sequences, t.shape[0])   # without a table there may be more pages than sequences
         self._ref = ctypes.addressof(c)
 
     def _check_slots(self, t, name):
         if t.dim() != 3 or t.shape[1] != self.kv_heads or t.shape[2] < self.slots or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous [B, kv_heads, slots] tensor of at least {self.slots} slots")
+        if self.table is not None and t.shape[0] < self.table.shape[0]:
+            raise ValueError(f"{name} must have a row for each of the table's {self.table.shape[0]} sequences (got {t.shape[0]})")
         return t
 
 
