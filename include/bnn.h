@@ -560,8 +560,9 @@ typedef struct bnn_attn_args {
                                                 strides multiples of 8          */
     int32_t out_dtype;                       /* BNN_F32 or the cache's dtype    */
     float* lse; int64_t ld_lse;              /* [rows, ld_lse >= heads] or NULL */
-    void* workspace; int64_t workspace_bytes;/* bnn_tree_attention_workspace bytes,
-                                                16-byte aligned                 */
+    void* workspace; int64_t workspace_bytes;/* bnn_tree_attention_workspace bytes, 16-byte
+                                                aligned; with fewer, or none, long sequences
+                                                are shared by fewer workgroups  */
 } bnn_attn_args;
 
 /* Attention of every new token over its sequence's committed tokens and the
@@ -578,7 +579,9 @@ typedef struct bnn_attn_args {
 bnn_status bnn_tree_attention(const bnn_kv_cache* cache, const bnn_kv_batch* batch,
                               const bnn_attn_args* args, bnn_stream_t stream);
 
-/* Workspace bytes of bnn_tree_attention (0 where it needs none); -1 for
+/* Workspace bytes with which bnn_tree_attention runs at its best (0 where it
+ * uses none), for this batch and for those of fewer sequences, new tokens,
+ * committed tokens or rows whose rows are at most their B * max_nodes; -1 for
  * arguments that it would refuse.  Device pointers are not looked at. */
 int64_t bnn_tree_attention_workspace(const bnn_kv_cache* cache, const bnn_kv_batch* batch, int64_t heads);
 

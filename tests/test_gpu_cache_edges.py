@@ -1,6 +1,6 @@
 """GPU checks of the calls over the paged key/value cache at the edges of their
 definitions: weights far below one that dominates its row, evictions where the
-recent tokens alone exceed the budget.
+recent tokens alone exceed the budget, workspaces made for other sizes.
 
 Bounds as in test_gpu_cache.py: u is half an ulp of a type as a ratio, products
 and sums in fp32 add (D + 10) 2^-24 sum |q k| scale to a logit and n 2^-24 to a
@@ -139,3 +139,35 @@ def test_evict_more_recent_tokens_than_the_budget(bnn, case, inplace):
                 wantK[(*to, h)], wantV[(*to, h)] = before[0][(*come, h)], before[1][(*come, h)]
     same = lambda x, y: torch.equal(x.contiguous().view(torch.int16), y.contiguous().view(torch.int16))
     assert same(cache.dK.cpu(), wantK) and same(cache.dV.cpu(), wantV)
+
+
+# ---- workspaces
+
+@pytest.mark.parametrize("heads,kv,dim,seqs,nodes,ctx", [(8, 2, 128, 64, 1, 1500), (8, 2, 64, 5, 70, 3000), (4, 4, 256, 3, 9, 2500)])
+def test_attention_with_a_workspace_of_other_sizes(bnn, heads, kv, dim, seqs, nodes, ctx):
+    """A workspace for more sequences and tokens, one that holds two chunks,
+    and none at all: the same function."""
+    banner(f"tree_attention workspaces {heads} {kv} {dim} {seqs} {nodes} {ctx}")
+    gen = torch.Generator(device="cuda").manual_seed(61)
+    normal = lambda *shape: torch.randn(shape, generator=gen, device="cuda").to(BF)
+    per = -(-(ctx + nodes) // 64)
+    table = torch.arange(seqs * per, dtype=torch.int32, device="cuda").reshape(seqs, per)
+    cache = bnn.KVCache(normal(seqs * per, 64, kv, dim), normal(seqs * per, 64, kv, dim), table)
+    work = bnn.tree_attention_workspace(cache, seqs * nodes, heads, nodes, ctx)
+    for b, n, spare in ((1, 1, 0), (1, nodes, 0), (seqs, 1, 3), (2, nodes, 300)):
+        rows = b * n
+        q = normal(rows + spare, heads, dim)
+        args = dict(max_nodes=n, max_ctx=ctx, out_dtype=torch.float32)
+        indptr, held = cuda_i32(range(0, rows + 1, n)), cuda_i32([ctx - 7 * i for i in range(b)])
+        two = torch.empty(2 * q.shape[0] * heads * (4 * dim + 8), dtype=torch.uint8, device="cuda")
+        results = [bnn.tree_attention(q, cache, indptr, held, workspace=w, **args) for w in (None, work, two, two[:0], two[:4096])]
+        # one row by its definition, the others alike.  A logit's products are off by (D + 10) 2^-24 scale sum |q k|, at most
+        # 266 x 6e-8 x 12 = 2e-4 here (normal values), a weight by as much again for lse, and the mean of |v| is 0.8
+        k, v = (x[table[0].long()].flatten(0, 1)[: ctx + 1].double() for x in (cache.k, cache.v))
+        for h in range(heads):
+            s = (k[:, h * kv // heads] @ q[0, h].double()) * dim ** -0.5
+            want = torch.softmax(s, 0) @ v[:, h * kv // heads]
+            for out, lse in results:
+                assert torch.allclose(out[0, h].double(), want, rtol=0, atol=4e-4) and abs(float(lse[0, h]) - float(torch.logsumexp(s, 0))) < 2e-4
+        for out, lse in results[1:]:
+            assert torch.allclose(out[:rows], results[0][0][:rows], rtol=0, atol=8e-4) and torch.allclose(lse[:rows], results[0][1][:rows], rtol=0, atol=4e-4)

@@ -812,8 +812,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCac
 
 
 def tree_attention_workspace(cache: KVCache, rows: int, heads: int, max_nodes: int, max_ctx: int) -> torch.Tensor:
-    """A workspace for tree_attention calls of up to these sizes over this
-    cache's sequences."""
+    """A workspace for tree_attention calls of up to these sizes over up to all
+    of this cache's sequences."""
     b = _pack_batch(0, 0, cache.sequences, rows, max_nodes, max_ctx)
     n = lib().bnn_tree_attention_workspace(cache._ref, b, heads)
     if n < 0:
@@ -831,7 +831,9 @@ def tree_attention(q: torch.Tensor, cache: KVCache, indptr: torch.Tensor, ctx: t
     [rows, words] (tree_mask), None for a causal run.  ``max_nodes`` and
     ``max_ctx`` bound the new and committed tokens of a sequence.  Returns
     (out [rows, heads, dim] in ``out_dtype``: float32, or the cache's type by
-    default; lse float32 [rows, heads], the logarithm of each row's sum)."""
+    default; lse float32 [rows, heads], the logarithm of each row's sum).
+    ``workspace``: tree_attention_workspace, made here where it is None; with
+    a smaller one long sequences are shared by fewer workgroups."""
     rows, heads, dim = q.shape
     b = _batch(cache, indptr, ctx, rows, max_nodes, max_ctx)
     if out is None:

@@ -221,9 +221,9 @@ bnn_status bnn_tree_attention(const bnn_kv_cache* cache, const bnn_kv_batch* bat
         if (a->ld_lse < a->heads) return BNN_ERR_LD;
         if (misaligned(a->lse, 4)) return BNN_ERR_ALIGN;
     }
-    const int64_t need = bnn::tree_attention_work(c, b, (int32_t)a->heads);
-    if (need < 0) return BNN_ERR_SHAPE;   // more workgroups than a launch takes
-    BNN_TRY(check_work(a->workspace, a->workspace_bytes, need));
+    if (a->workspace_bytes < 0) return BNN_ERR_SHAPE;
+    BNN_TRY(check_work(a->workspace, a->workspace_bytes, a->workspace_bytes));
+    if (!bnn::tree_attention_fits(c, b, (int32_t)a->heads, a->workspace_bytes)) return BNN_ERR_SHAPE;   // more workgroups than a launch takes
     if (b.rows == 0 || b.B == 0 || b.max_nodes == 0) return BNN_OK;
     bnn::AttnArgs r;
     r.q = (const char*)a->q; r.q_row = 2 * a->q_row; r.q_head = 2 * a->q_head;
@@ -232,7 +232,7 @@ bnn_status bnn_tree_attention(const bnn_kv_cache* cache, const bnn_kv_batch* bat
     r.scale = a->scale;
     r.out = (char*)a->out; r.o_row = obytes * a->o_row; r.o_head = obytes * a->o_head;
     r.lse = a->lse; r.ld_lse = a->ld_lse;
-    r.work = (char*)a->workspace;
+    r.work = (char*)a->workspace; r.work_bytes = a->workspace_bytes;
     return from_hip(bnn::launch_tree_attention(c, b, r, cache->dtype, a->out_dtype, as_stream(stream)));
 }
 

@@ -31,9 +31,10 @@ struct AttnArgs {
     float scale;
     char* out; int64_t o_row, o_head;       // strides in bytes
     float* lse; int64_t ld_lse;
-    char* work;
+    char* work; int64_t work_bytes;
 };
 
+bool tree_attention_fits(const KvCache& c, const KvBatch& b, int32_t heads, int64_t work_bytes);   // a launch takes the grid
 // Workspace bytes; -1 where a launch would not take the grid.
 int64_t tree_attention_work(const KvCache& c, const KvBatch& b, int32_t heads);
 hipError_t launch_tree_attention(const KvCache& c, const KvBatch& b, const AttnArgs& a, int32_t dtype, int32_t out_dtype,
