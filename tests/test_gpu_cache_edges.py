@@ -1,6 +1,7 @@
 """GPU checks of the calls over the paged key/value cache at the edges of their
 definitions: weights far below one that dominates its row, evictions where the
-recent tokens alone exceed the budget, workspaces made for other sizes.
+recent tokens alone exceed the budget, workspaces made for other sizes, steps without
+new tokens.
 
 Bounds as in test_gpu_cache.py: u is half an ulp of a type as a ratio, products
 and sums in fp32 add (D + 10) 2^-24 sum |q k| scale to a logit and n 2^-24 to a
@@ -171,3 +172,58 @@ def test_attention_with_a_workspace_of_other_sizes(bnn, heads, kv, dim, seqs, no
                 assert torch.allclose(out[0, h].double(), want, rtol=0, atol=4e-4) and abs(float(lse[0, h]) - float(torch.logsumexp(s, 0))) < 2e-4
         for out, lse in results[1:]:
             assert torch.allclose(out[:rows], results[0][0][:rows], rtol=0, atol=8e-4) and torch.allclose(lse[:rows], results[0][1][:rows], rtol=0, atol=4e-4)
+
+
+# ---- nothing to do
+
+def no_tokens(B, kv=2, heads=4, dim=64, n=40):
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    normal = lambda *shape: torch.randn(shape, generator=gen, device="cuda")
+    per = -(-n // 16)
+    K, V = normal(B * per + 1, 16, kv, dim).to(BF), normal(B * per + 1, 16, kv, dim).to(BF)
+    pos = torch.stack([torch.randperm(per * 16, generator=gen, device="cuda") for _ in range(B * kv)]) if B else torch.empty(0, device="cuda")
+    return (K, V, torch.arange(B * per, dtype=torch.int32, device="cuda").reshape(B, per), pos.to(torch.int32).reshape(B, kv, per * 16).contiguous(),
+            normal(B, kv, per * 16).abs())
+
+
+@pytest.mark.parametrize("B", [0, 3])
+def test_a_step_without_new_tokens(bnn, B):
+    """No rows (every sequence waits), and no sequences: the calls do what is
+    left to do, which for the sums is the copy and for the eviction the cut."""
+    banner(f"no rows, {B} sequences")
+    K, V, table, pos, score = no_tokens(B)
+    kept = [x.clone() for x in (K, V, pos, score)]
+    cache = bnn.KVCache(K, V, table, pos=pos, score=score)
+    indptr, ctx = cuda_i32([0] * (B + 1)), cuda_i32([40] * B)
+    q, k = torch.empty((0, 4, 64), device="cuda"), torch.empty((0, 2, 64), device="cuda")
+    qr = bnn.qk_norm_rope(q, k, k, cache, indptr, ctx, cuda_i32([]), bnn.rope_turns(50, 64, device="cuda"))
+    assert qr.shape == (0, 4, 64) and qr.dtype == BF
+    mask, accept = torch.empty((0, 1), dtype=torch.int32, device="cuda"), torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+    args = dict(max_nodes=5, max_ctx=40)
+    out, lse = bnn.tree_attention(qr, cache, indptr, ctx, mask=mask, **args)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    res = torch.full_like(score, 9.0)
+    assert bnn.cache_score_add(qr, lse, cache, indptr, ctx, mask=mask, accept=accept, score_out=res, **args) is res and torch.equal(res, score)
+    bnn.cache_score_add(qr, lse, cache, indptr, ctx, **args)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip((K, V, pos, score), kept))
+    got = bnn.cache_evict(cache, indptr, ctx, budget=25, recent=0, accept=accept, **args)
+    assert got.tolist() == [25] * B
+    for b in range(B):
+        for h in range(2):
+            source = evict_by_rank(40, np.zeros(0, dtype=bool), 25, 0, kept[2][b, h].cpu().numpy(), kept[3][b, h].cpu().numpy())
+            assert np.array_equal(pos[b, h, :25].cpu().numpy(), kept[2][b, h].cpu().numpy()[source]) and (pos[b, h, 25:40] == -1).all()
+
+
+def test_no_pages_and_no_table_of_angles(bnn):
+    """A cache without pages holds nothing; a table without positions gives NaN."""
+    banner("no pages")
+    K = torch.empty((0, 16, 2, 64), dtype=BF, device="cuda")
+    cache = bnn.KVCache(K, K.clone(), torch.zeros((2, 3), dtype=torch.int32, device="cuda"))
+    q, k = torch.randn((2, 4, 64), device="cuda"), torch.randn((2, 2, 64), device="cuda")
+    indptr, ctx = cuda_i32([0, 1, 2]), cuda_i32([0, 5])
+    qr = bnn.qk_norm_rope(q, k, k, cache, indptr, ctx, cuda_i32([0, 1]), bnn.rope_turns(0, 32, device="cuda"))
+    assert qr[..., :32].isnan().all() and torch.equal(qr[..., 32:], q[..., 32:].to(BF))
+    out, lse = bnn.tree_attention(q.to(BF), cache, indptr, ctx, max_nodes=1, max_ctx=5)
+    # missing pages read as rows of zeros: logits 0, values 0
+    assert (out == 0).all() and torch.allclose(lse, torch.tensor([[0.0] * 4, [6.0] * 4], device="cuda").clamp(min=1).log(), rtol=0, atol=1e-6)

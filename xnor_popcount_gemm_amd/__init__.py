@@ -641,6 +641,11 @@ _pack_batch, _pack_rope, _pack_attn, _pack_score, _pack_evict = (
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# Address of tensors without elements (a step without new tokens, a batch
+# without sequences): torch gives them none, and the C calls want one though
+# they do not read it.
+_EMPTY = 256
+
 BF16, F16, F32 = 1, 2, 3
 _KV_TYPES = {torch.bfloat16: BF16, torch.float16: F16}
 ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
@@ -672,13 +677,13 @@ class KVCache:
         self._index = k.device.index
         self.kv_heads, self.dim, self.page_size = heads, dim, page
         c = self._c = _KvCache()
-        c.K, c.k_page, c.k_slot, c.k_head = k.data_ptr(), k.stride(0), k.stride(1), k.stride(2)
-        c.V, c.v_page, c.v_slot, c.v_head = v.data_ptr(), v.stride(0), v.stride(1), v.stride(2)
+        c.K, c.k_page, c.k_slot, c.k_head = k.data_ptr() or _EMPTY, k.stride(0), k.stride(1), k.stride(2)
+        c.V, c.v_page, c.v_slot, c.v_head = v.data_ptr() or _EMPTY, v.stride(0), v.stride(1), v.stride(2)
         if table is not None:
             _dev(table, torch.int32, "table")
             if table.dim() != 2 or not table.is_contiguous():
                 raise ValueError("table must be a contiguous [B, pages per sequence] tensor")
-            c.table, c.ld_table = table.data_ptr(), table.shape[1]
+            c.table, c.ld_table = table.data_ptr() or _EMPTY, table.shape[1]
         c.num_pages, c.page_size, c.kv_heads, c.dim, c.dtype = pages, page, heads, dim, _KV_TYPES[k.dtype]
         self.sequences = pages if table is None else table.shape[0]
         self.slots = page if table is None else table.shape[1] * page
@@ -703,7 +708,7 @@ def _batch(cache: KVCache, indptr, ctx, rows: int, max_nodes: int, max_ctx: int)
         _dev(indptr, torch.int32, "indptr")
         _dev(ctx, torch.int32, "ctx")
         raise ValueError("indptr must be [B + 1] and ctx [B], contiguous, for at most the cache's sequences")
-    return _pack_batch(indptr.data_ptr(), ctx.data_ptr(), n, rows, max_nodes, max_ctx)
+    return _pack_batch(indptr.data_ptr(), ctx.data_ptr() or _EMPTY, n, rows, max_nodes, max_ctx)
 
 
 def _token_rows(t: torch.Tensor, dtype, name: str, rows, heads, dim):
@@ -712,21 +717,21 @@ def _token_rows(t: torch.Tensor, dtype, name: str, rows, heads, dim):
     if not (t.dtype is dtype and t.is_cuda and t.shape == (rows, heads, dim) and st[2] == 1):
         _dev(t, dtype, name)
         raise ValueError(f"{name} must be [{rows}, {heads}, {dim}] with a unit last stride (got {tuple(t.shape)})")
-    return t.data_ptr(), st[0], st[1]
+    return t.data_ptr() or _EMPTY, st[0], st[1]
 
 
 def _flat(t: torch.Tensor, dtype, name: str, n: int) -> int:
     if not (t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous()):
         _dev(t, dtype, name)
         raise ValueError(f"{name} must be contiguous, with {n} elements")
-    return t.data_ptr()
+    return t.data_ptr() or _EMPTY
 
 
 def _row_floats(t: torch.Tensor, name: str, rows: int, heads: int):
     if not (t.dtype is torch.float32 and t.is_cuda and t.shape == (rows, heads) and t.stride(1) == 1):
         _dev(t, torch.float32, name)
         raise ValueError(f"{name} must be [{rows}, {heads}] with a unit last stride")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr() or _EMPTY, t.stride(0)
 
 
 def _bit_rows(t: torch.Tensor | None, name: str, rows: int):
@@ -735,7 +740,7 @@ def _bit_rows(t: torch.Tensor | None, name: str, rows: int):
     if not (t.dtype is torch.int32 and t.is_cuda and t.dim() == 2 and t.shape[0] == rows and t.is_contiguous()):
         _dev(t, torch.int32, name)
         raise ValueError(f"{name} must be a contiguous packed int32 [{rows}, words] tensor")
-    return t.data_ptr(), t.shape[1]
+    return t.data_ptr() or _EMPTY, t.shape[1]
 
 
 def rope_turns(max_pos: int, rot: int, *, base: float = 10000.0, kind: str = "plain", factor: float = 1.0,
@@ -747,7 +752,7 @@ def rope_turns(max_pos: int, rot: int, *, base: float = 10000.0, kind: str = "pl
     t = torch.empty((int(max_pos), int(rot)), dtype=torch.float32)
     if kind not in ROPE_KINDS:
         raise ValueError(f"kind must be one of {sorted(ROPE_KINDS)}")
-    _check(lib().bnn_rope_turns_host(max_pos, rot, base, ROPE_KINDS[kind], factor, old_ctx, beta_fast, beta_slow, _ptr(t)),
+    _check(lib().bnn_rope_turns_host(max_pos, rot, base, ROPE_KINDS[kind], factor, old_ctx, beta_fast, beta_slow, _ptr(t) or _EMPTY),
            "bnn_rope_turns_host")
     return t if device is None else t.to(device)
 
@@ -795,11 +800,11 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCac
         table = _flat(turns, torch.float32, "turns", max_pos * rot)
     pos, score, slots = 0, 0, 0
     if cache.pos is not None:
-        pos, slots = cache.pos.data_ptr(), cache.pos.shape[2]
+        pos, slots = cache.pos.data_ptr() or _EMPTY, cache.pos.shape[2]
     if cache.score is not None:
         if pos and slots != cache.score.shape[2]:
             raise ValueError("cache.pos and cache.score must have the same number of slots")
-        score, slots = cache.score.data_ptr(), cache.score.shape[2]
+        score, slots = cache.score.data_ptr() or _EMPTY, cache.score.shape[2]
     a = _pack_rope(*_token_rows(q, src, "q", rows, heads, dim), *_token_rows(k, src, "k", rows, kv, dim),
                    *_token_rows(v, src, "v", rows, kv, dim), F32 if src is torch.float32 else _KV_TYPES[src], heads,
                    *_token_rows(q_out, cache.dtype, "q_out", rows, heads, dim),
@@ -871,7 +876,7 @@ def cache_score_add(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, indptr: 
         raise ValueError("score_out must be laid out as cache.score")
     a = _pack_score(*_token_rows(q, cache.dtype, "q", rows, heads, cache.dim), heads, *_row_floats(lse, "lse", rows, heads),
                     *_bit_rows(mask, "mask", rows), *_bit_rows(accept, "accept", ctx.numel()), dim ** -0.5 if scale is None else scale,
-                    cache.score.data_ptr(), score_out.data_ptr(), cache.score.shape[2])
+                    cache.score.data_ptr() or _EMPTY, score_out.data_ptr() or _EMPTY, cache.score.shape[2])
     _check((_lib or lib()).bnn_cache_score_add(cache._ref, _batch(cache, indptr, ctx, rows, max_nodes, max_ctx), a, _raw_stream(cache._index)),
            "bnn_cache_score_add")
     return score_out
@@ -908,8 +913,8 @@ def cache_evict(cache: KVCache, indptr: torch.Tensor, ctx: torch.Tensor, *, budg
         raise ValueError("ctx_out must be laid out as ctx")
     if workspace is None:
         workspace = cache_evict_workspace(cache)
-    a = _pack_evict(*_bit_rows(accept, "accept", ctx.numel()), budget, recent, cache.pos.data_ptr(), pos_out.data_ptr(),
-                    cache.score.data_ptr(), score_out.data_ptr(), slots[2], ctx_out.data_ptr(), workspace.data_ptr(),
+    a = _pack_evict(*_bit_rows(accept, "accept", ctx.numel()), budget, recent, cache.pos.data_ptr() or _EMPTY, pos_out.data_ptr() or _EMPTY,
+                    cache.score.data_ptr() or _EMPTY, score_out.data_ptr() or _EMPTY, slots[2], ctx_out.data_ptr() or _EMPTY, workspace.data_ptr(),
                     workspace.numel() * workspace.element_size())
     _check((_lib or lib()).bnn_cache_evict(cache._ref, _batch(cache, indptr, ctx, 1 << 30, max_nodes, max_ctx), a, _raw_stream(cache._index)),
            "bnn_cache_evict")
