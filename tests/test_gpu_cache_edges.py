@@ -1,7 +1,7 @@
 """GPU checks of the calls over the paged key/value cache at the edges of their
 definitions: weights far below one that dominates its row, evictions where the
 recent tokens alone exceed the budget, workspaces made for other sizes, steps without
-new tokens.
+new tokens, infinities among the committed tokens.
 
 Bounds as in test_gpu_cache.py: u is half an ulp of a type as a ratio, products
 and sums in fp32 add (D + 10) 2^-24 sum |q k| scale to a logit and n 2^-24 to a
@@ -227,3 +227,48 @@ def test_no_pages_and_no_table_of_angles(bnn):
     out, lse = bnn.tree_attention(q.to(BF), cache, indptr, ctx, max_nodes=1, max_ctx=5)
     # missing pages read as rows of zeros: logits 0, values 0
     assert (out == 0).all() and torch.allclose(lse, torch.tensor([[0.0] * 4, [6.0] * 4], device="cuda").clamp(min=1).log(), rtol=0, atol=1e-6)
+
+
+# ---- infinities among the committed tokens
+
+@pytest.mark.parametrize("kind", [BF, FP], ids=["bf16", "f16"])
+@pytest.mark.parametrize("T,heads,kv,dim", [(1, 4, 1, 128), (1, 2, 2, 64), (9, 8, 2, 96), (70, 16, 2, 64), (3, 8, 1, 256)])
+def test_score_of_infinite_keys(bnn, T, heads, kv, dim, kind):
+    """Committed keys that hold an infinity: a logit of -inf adds nothing, one
+    of +inf adds infinity, NaN adds NaN; rows that are not there and rows that
+    saw nothing add nothing to either."""
+    banner(f"cache_score_add infinite keys T={T} {kind}")
+    rng = np.random.default_rng(81)
+    n, g, scale = 150, heads // kv, dim ** -0.5
+    cache = ref.Paged(rng, 1, n + T, 16, kv, dim, kind)
+    k = rng.standard_normal((n + T, kv, dim))
+    k[40, :, 3], k[41, :, 3], k[70, :, 3], k[71, 0, 5] = -np.inf, np.inf, -np.inf, np.nan
+    cache.put("K", 0, np.arange(n + T), k)
+    cache.put("V", 0, np.arange(n + T), np.zeros((n + T, kv, dim)))
+    q = torch.from_numpy(rng.standard_normal((T, heads, dim)) * 0.5)
+    q[..., 3] = q[..., 3].abs() + 0.25
+    q = q.to(kind)
+    lse = torch.from_numpy(rng.standard_normal((T, heads)) + 4).float()
+    lse[0, 0] = float("-inf")
+    score = torch.from_numpy(rng.random((1, kv, cache.slots))).float()
+    dc = cache.device(bnn, score=score.cuda())
+    got = bnn.cache_score_add(q.cuda(), lse.cuda(), dc, cuda_i32([0, T]), cuda_i32([n]), max_nodes=T, max_ctx=n, scale=scale).double().cpu().numpy()[0]
+    k = cache.get("K", 0, np.arange(n + T))
+    want, tol = score[0, :, : n + T].double().numpy().copy(), np.zeros((kv, n + T))
+    with np.errstate(invalid="ignore"):
+        for i in range(T):
+            for h in range(heads):
+                if not torch.isneginf(lse[i, h]):
+                    x = k[: n + i + 1, h // g] @ q[i, h].double().numpy() * scale
+                    S = np.abs(k[: n + i + 1, h // g]) @ np.abs(q[i, h].double().numpy()) * scale
+                    w = np.exp(x - float(lse[i, h]))
+                    want[h // g, : n + i + 1] += w
+                    finite = np.isfinite(x)
+                    tol[h // g, : n + i + 1][finite] += (w * ((dim + 10) * S + 8 * np.abs(x) + 8 * abs(float(lse[i, h])) + 8 + T * g) * ref.E32)[finite]
+    assert np.isfinite(want[:, 40]).all()
+    if T * g > 1:                               # else head 0 has the one row that saw nothing
+        assert np.isnan(want[0, 71]) and np.isinf(want[:, 41]).all()
+    got = got[:, : n + T]
+    finite = np.isfinite(want)
+    assert np.array_equal(got[~finite], want[~finite], equal_nan=True)
+    assert (np.abs(got[finite] - want[finite]) <= (tol + 2 * ref.E32 * np.abs(want))[finite]).all()

@@ -14,6 +14,11 @@
 // A lane holds one slot's products with 4 rows, so the sum over rows runs in
 // registers and two lane swaps finish it; no atomics, a fixed order.
 //
+// Places without a row hold Q = 0 and lse = +inf, which gives a weight of 0
+// unless K holds an infinity or NaN, and so does lse = -inf of a row that saw
+// nothing.  A sum that is not finite is therefore taken again row by row by
+// what each sees, as in the tiles that hold new tokens.
+//
 // The grid is what fits the chip at once, and each wave takes an equal run of
 // all tiles in the order sequence, key head, tile: sequences of any lengths
 // are balanced, and a wave's start (page lookup, list of rows, Q) is paid once
@@ -182,7 +187,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
                 if ((lane & 3) == 0) {
                     const float lse = live ? a.lse[row * a.ld_lse + head] * 1.44269504088896340736f : INFINITY;
                     lows[wave][16 * g + qr] = lse == -INFINITY ? INFINITY : lse;
-                    node_of[wave][16 * g + qr] = live ? node : -1;
+                    node_of[wave][16 * g + qr] = live && lse != -INFINITY ? node : -1;
                 }
             }
         };
@@ -191,10 +196,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
         auto sight = [&](int64_t s0) {
             if (lane < ROWS) {
                 const int node = node_of[wave][lane];
-                const int64_t rel = s0 - sq.ctx;   // above -32
+                const int64_t rel = s0 - sq.ctx;
                 uint32_t vis = 0;
                 if (node >= 0) {
-                    if (!a.mask) {
+                    if (rel <= -32) {
+                        vis = ~0u;
+                    } else if (!a.mask) {
                         const int64_t n = node - rel + 1;
                         vis = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
                     } else {
@@ -242,43 +249,48 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
                     next = before(t + 1);
                     if (t + 2 < end) locate(t + 2);
                 }
-                const bool masked = s0 + 32 > sq.ctx;
-                float sum[NB] = {};
+                float sum[NB];
 #pragma unroll 1
-                for (int n0 = 0; n0 < nodes; n0 += 64) {
-                    const int rows = few ? first : list(n0);
-#pragma unroll 1
-                    for (int r0 = 0; r0 < rows; r0 += ROWS) {
-                        if (!few) {
-                            stage(r0, rows);
-                            wait_all();
-                        }
-                        if (masked) sight(s0);
-#pragma unroll 1
-                        for (int g = 0; g < 2 && r0 + 16 * g < rows; ++g) {
-                            f32x4 x[NB] = {};
+                for (bool masked = s0 + 32 > sq.ctx;; masked = true) {
 #pragma unroll
-                            for (int s = 0; s < QS; ++s) {
-                                const vec8 q = *(const vec8*)(qread + g * GRP + 1024 * s);
-#pragma unroll
-                                for (int n = 0; n < NB; ++n) x[n] = mma16(q, k[n][s], x[n]);
+                    for (int n = 0; n < NB; ++n) sum[n] = 0.f;
+#pragma unroll 1
+                    for (int n0 = 0; n0 < nodes; n0 += 64) {
+                        const int rows = few ? first : list(n0);
+#pragma unroll 1
+                        for (int r0 = 0; r0 < rows; r0 += ROWS) {
+                            if (!few) {
+                                stage(r0, rows);
+                                wait_all();
                             }
-                            const f32x4 low = *(const f32x4*)&lows[wave][16 * g + 4 * quad];
+                            if (masked) sight(s0);
+#pragma unroll 1
+                            for (int g = 0; g < 2 && r0 + 16 * g < rows; ++g) {
+                                f32x4 x[NB] = {};
 #pragma unroll
-                            for (int n = 0; n < NB; ++n)
+                                for (int s = 0; s < QS; ++s) {
+                                    const vec8 q = *(const vec8*)(qread + g * GRP + 1024 * s);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) x[n][i] = __builtin_amdgcn_exp2f(fmaf(x[n][i], c2, -low[i]));
-                            if (masked) {
-                                const u32x4 v = *(const u32x4*)&vis_of[wave][16 * g + 4 * quad];
+                                    for (int n = 0; n < NB; ++n) x[n] = mma16(q, k[n][s], x[n]);
+                                }
+                                const f32x4 low = *(const f32x4*)&lows[wave][16 * g + 4 * quad];
 #pragma unroll
                                 for (int n = 0; n < NB; ++n)
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) x[n][i] = (v[i] >> (16 * n + col)) & 1u ? x[n][i] : 0.f;
-                            }
+                                    for (int i = 0; i < 4; ++i) x[n][i] = __builtin_amdgcn_exp2f(fmaf(x[n][i], c2, -low[i]));
+                                if (masked) {
+                                    const u32x4 v = *(const u32x4*)&vis_of[wave][16 * g + 4 * quad];
 #pragma unroll
-                            for (int n = 0; n < NB; ++n) sum[n] += (x[n][0] + x[n][1]) + (x[n][2] + x[n][3]);
+                                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) x[n][i] = (v[i] >> (16 * n + col)) & 1u ? x[n][i] : 0.f;
+                                }
+#pragma unroll
+                                for (int n = 0; n < NB; ++n) sum[n] += (x[n][0] + x[n][1]) + (x[n][2] + x[n][3]);
+                            }
                         }
                     }
+                    if (masked || !__any(!(fabsf(sum[0]) < INFINITY) || !(fabsf(sum[1]) < INFINITY))) break;
                 }
                 done = old + over_rows(sum[0], sum[1]);
             }
