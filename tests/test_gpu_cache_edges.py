@@ -1,7 +1,7 @@
 """GPU checks of the calls over the paged key/value cache at the edges of their
 definitions: weights far below one that dominates its row, evictions where the
 recent tokens alone exceed the budget, workspaces made for other sizes, steps without
-new tokens, infinities among the committed tokens.
+new tokens, infinities and NaN among the committed tokens.
 
 Bounds as in test_gpu_cache.py: u is half an ulp of a type as a ratio, products
 and sums in fp32 add (D + 10) 2^-24 sum |q k| scale to a logit and n 2^-24 to a
@@ -272,3 +272,39 @@ def test_score_of_infinite_keys(bnn, T, heads, kv, dim, kind):
     finite = np.isfinite(want)
     assert np.array_equal(got[~finite], want[~finite], equal_nan=True)
     assert (np.abs(got[finite] - want[finite]) <= (tol + 2 * ref.E32 * np.abs(want))[finite]).all()
+
+
+# ---- NaN logits
+
+@pytest.mark.parametrize("out", [BF, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,heads,kv,dim,ctx", [(1, 4, 1, 128, 60), (1, 4, 1, 128, 5000), (7, 8, 2, 64, 5000), (15, 8, 2, 96, 900), (40, 8, 2, 128, 5000),
+                                                (40, 8, 2, 256, 3000)])
+def test_attention_of_nan_rows(bnn, T, heads, kv, dim, ctx, out):
+    """A query that holds NaN gives NaN in its row and head alone; NaN in the
+    keys of a whole run of committed slots gives it to every row of that key
+    head; however many chunks the slots are cut into."""
+    banner(f"tree_attention NaN T={T} dim={dim} ctx={ctx} {out}")
+    rng = np.random.default_rng(91)
+    cache = ref.Paged(rng, 1, ctx + T, 16, kv, dim, BF)
+    for w in "KV":
+        cache.put(w, 0, np.arange(ctx + T), rng.standard_normal((ctx + T, kv, dim)))
+    q = torch.from_numpy(rng.standard_normal((T, heads, dim))).to(BF)
+    args = dict(max_nodes=T, max_ctx=ctx, out_dtype=out)
+    run = lambda q: bnn.tree_attention(q.cuda(), cache.device(bnn), cuda_i32([0, T]), cuda_i32([ctx]), **args)
+    whole, lse0 = run(q)
+    assert not whole.isnan().any() and not lse0.isnan().any()
+    bad = q.clone()
+    bad[T // 2, 1, 5] = float("nan")
+    got, lse = run(bad)
+    assert got[T // 2, 1].isnan().all() and lse[T // 2, 1].isnan()
+    rest = torch.ones(T, heads, dtype=torch.bool)
+    rest[T // 2, 1] = False
+    assert torch.equal(got.cpu()[rest], whole.cpu()[rest]) and torch.equal(lse.cpu()[rest], lse0.cpu()[rest])
+    first = np.arange(min(ctx, 300))
+    k = cache.get("K", 0, first)
+    k[:, 0, 2] = np.nan
+    cache.put("K", 0, first, k)
+    got, lse = run(q)
+    g = heads // kv
+    assert got[:, :g].isnan().all() and lse[:, :g].isnan().all()
+    assert torch.equal(got[:, g:], whole[:, g:]) and torch.equal(lse[:, g:], lse0[:, g:])

@@ -558,6 +558,7 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
 
     // join the slot groups of the workgroup, then write rows
     l = row_sum<R>(l);
+    if (l != l) m = INFINITY;   // NaN among the logits: outweighs the other slot groups and chunks, whatever the maximum here
     const bool last = nchunk == 1;
     const int64_t prow = part_rows(b.rows, a.heads);
     float* const pout = (float*)a.work;
