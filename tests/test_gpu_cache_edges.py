@@ -308,3 +308,47 @@ def test_attention_of_nan_rows(bnn, T, heads, kv, dim, ctx, out):
     g = heads // kv
     assert got[:, :g].isnan().all() and lse[:, :g].isnan().all()
     assert torch.equal(got[:, g:], whole[:, g:]) and torch.equal(lse[:, g:], lse0[:, g:])
+
+
+# ---- infinities among the committed values
+
+@pytest.mark.parametrize("out", ["same", "f32"])
+@pytest.mark.parametrize("kind", [BF, FP], ids=["bf16", "f16"])
+@pytest.mark.parametrize("T,heads,kv,dim,ctx,page", [(1, 4, 2, 128, 40, 16), (1, 4, 2, 64, 3000, 16), (7, 8, 2, 96, 1500, 1), (15, 8, 2, 128, 700, 24),
+                                                     (40, 8, 2, 128, 3000, 64), (200, 4, 2, 64, 300, 64), (20, 8, 2, 256, 900, 16), (2, 8, 2, 256, 2000, 16)])
+def test_attention_of_infinite_values(bnn, T, heads, kv, dim, ctx, page, kind, out):
+    """Values that hold infinities of one sign, of both, and NaN give
+    infinity or NaN in that dimension to every row, however small their weight
+    (the last of them lie 100 below the largest logit); other dimensions are
+    as the definition says."""
+    banner(f"tree_attention infinite values T={T} dim={dim} ctx={ctx} {kind} {out}")
+    rng = np.random.default_rng(101)
+    n, scale = ctx + T, dim ** -0.5
+    out = kind if out == "same" else torch.float32
+    cache = ref.Paged(rng, 1, n, page, kv, dim, kind)
+    direction = np.sign(rng.standard_normal(dim))
+    k, v = rng.standard_normal((2, n, kv, dim)) * np.array([0.5, 1.0])[:, None, None, None]
+    far = ctx - 3
+    k[far] = -direction * (100 / (dim * scale))
+    inf = np.inf
+    v[5, :, 7], v[ctx // 2, :, 11], v[ctx // 3, :, 12], v[ctx // 3 + 1, :, 12], v[9, :, 13] = inf, -inf, inf, -inf, np.nan
+    v[far, :, 14], v[far, :, dim - 1], v[far - 1, 0, 20] = inf, -inf, inf
+    v[ctx + T // 2, 1, 22], v[ctx, 0, 23], v[ctx + T - 1, :, 24] = -inf, inf, np.nan    # new tokens that some rows see
+    for w, x in (("K", k), ("V", v)):
+        cache.put(w, 0, np.arange(n), x)
+    q = torch.from_numpy(direction + 0.3 * rng.standard_normal((T, heads, dim))).to(kind)
+    got, lse = bnn.tree_attention(q.cuda(), cache.device(bnn), cuda_i32([0, T]), cuda_i32([ctx]), max_nodes=T, max_ctx=ctx, scale=scale, out_dtype=out)
+    torch.cuda.synchronize()
+    got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
+    k, v = (cache.get(w, 0, np.arange(n)) for w in "KV")
+    u = ref.U[out] + (ref.U[kind] if out == kind else 2.0 ** -22) + 2.0 ** -24
+    for i in range(T):
+        with np.errstate(invalid="ignore"):
+            y, l, A, S = ref.attention(q[i].double().numpy(), k, v, ref.sees(ctx, T, i, None), scale)
+        assert np.isposinf(y[:, [7, 14]]).all() and np.isneginf(y[:, [11, dim - 1]]).all() and np.isnan(y[:, 12:14]).all() and np.isposinf(y[0, 20])
+        odd = ~np.isfinite(y)
+        assert np.array_equal(got[i][odd], y[odd], equal_nan=True), i
+        ds = (dim + 10) * ref.E32 * S
+        assert (np.abs(lse[i] - l) <= ds + (n + 8) * ref.E32 + 8 * ref.E32 * np.abs(l)).all()
+        bound = u * np.where(odd, 0, A) + (2 * ds + 2 * n * ref.E32)[:, None] * np.where(odd, 0, A) + 2.0 ** -24
+        assert (np.abs(got[i][~odd] - y[~odd]) <= bound[~odd]).all(), i

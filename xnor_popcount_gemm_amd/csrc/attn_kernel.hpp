@@ -37,12 +37,18 @@
 // (transposed reads of two pieces of 4 slots).  Rows past the end are read
 // from a block of zeros.
 //
-// Masks.  Committed slots are seen by every row and cost nothing; steps that
-// hold new tokens take one 32-bit word per row and 32 slots, and run as the
-// others do where every row sees them whole (a causal run below its diagonal).  An unseen token must not matter even where its V is NaN
-// or infinite, and 0 * NaN is NaN, so a masked step takes such values as 0 in
+// Masks.  Committed slots are seen by every row and cost nothing, and so do the
+// new tokens of a causal run up to the first row's own (a prompt of 4096 tokens:
+// 182 us; 212 with these steps among the masked ones).  Steps that hold other
+// new tokens take one 32-bit word per row and 32 slots, and run as the others do
+// where every row sees them whole.  An unseen token must not matter even where
+// its V is NaN or infinite, and 0 * NaN is NaN, so a masked step takes such values as 0 in
 // the products and notes, as bits per row and dimension, which rows saw an
-// infinity of which sign (NaN: both); the infinities are added at the end.
+// infinity of which sign (NaN: both); the infinities are added at the end.  A
+// plain step has no such care: a weight that was rounded to 0, or the negative
+// remainder of one, makes NaN of a committed infinity.  Where a wave's result is
+// not finite it reads V of the slots that all rows see once more for what they
+// hold.
 // What bounds it.  Few rows: the read of K and V; 285 us for 1.59 GB, where the
 // same paged rows fetched and not used take about 265.  Many rows: neither the
 // matrix cores (busy 39% of the time at a 1024-token chunk, 790 TFLOP/s) nor
@@ -102,6 +108,12 @@ __device__ __forceinline__ float row_sum(float x) {
         x = __uint_as_float(q[0]) + __uint_as_float(q[1]);
     }
     return x;
+}
+
+// Factor of sums taken relative to m where they join others relative to M.  Never 0 but where nothing was
+// seen: infinities stay infinities.
+__device__ __forceinline__ float joined(float m, float M) {
+    return m == -INFINITY ? 0.f : fmaxf(__builtin_amdgcn_exp2f(m - M), 0x1p-126f);
 }
 
 template <int R> struct Acc;
@@ -469,8 +481,10 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
         }
     };
 
-    // steps whose slots are all committed and inside the chunk, then the others
-    const int sure = k1 < sq.ctx ? k1 : sq.ctx;
+    // Slots of the chunk that all rows see: the committed ones; of a causal run also the new tokens up to the first row's own.
+    const int64_t shared = (int64_t)sq.ctx + (a.mask ? 0 : tile0 / a.group + 1);
+    const int sure = k1 < shared ? k1 : (int)shared;
+    // steps of these alone, then the others
     int plain = sure > k0 ? (sure - k0) / (KW * A::BN) : 0;
     plain = plain < steps ? plain : steps;
     if (steps > 0) {
@@ -540,25 +554,59 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
             else if (seen != 0) work(std::true_type{}, buf, vis, nullptr, nullptr);
         }
     }
+    l = row_sum<R>(l);
+    if (l != l) m = INFINITY;   // NaN among the logits: outweighs the other slot groups and chunks, whatever the maximum here
     {
+        float odd = 0.f;   // NaN where a result is not finite
+#pragma unroll
+        for (int i = 0; i < A::OB; ++i)
+#pragma unroll
+            for (int e = 0; e < (int)(sizeof(acc) / 4); ++e) odd = fmaf(o[i][e], 0.f, odd);
         uint32_t any = 0;
 #pragma unroll
         for (int w = 0; w < A::PW; ++w) any |= plus[w] | minus[w];
-        if (__any(any)) {
+        if (__any(any || odd != odd)) {
+            // of the slots that all rows see, 16-byte pieces of several at a time; bits 0-7: +inf or NaN in that dimension, 8-15: -inf or NaN
+            constexpr int PER = D / 8, ROWS = 64 / PER;
+            const int piece = lane % PER;
+            const char* const base = vbase - (fp ^ A::B::v_swap(fr)) * 16 + piece * 16;
+            uint32_t found = 0;
+            if (lane < PER * ROWS) {
+#pragma unroll 4
+                for (int s = k0 + lane / PER; s < sure; s += ROWS) {
+                    const uint32_t p = fastdiv(s, c.page);
+                    const int32_t page = table ? table[p] : seq;
+                    const u32x4 x = *(const u32x4*)((uint32_t)page < c.num_pages ? base + page * c.v_page + (s - p * c.page.d) * c.v_slot : (const char*)zero_row);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t h = x[e / 2] >> (16 * (e & 1)) & 0xFFFFu;
+                        const bool nan = (h & 0x7FFFu) > T::special;
+                        found |= (uint32_t)(nan || h == T::special) << e | (uint32_t)(nan || h == (T::special | 0x8000u)) << (8 + e);
+                    }
+                }
+            }
+            uint32_t all = 0;   // lane p: of dimensions 8 p ..
+#pragma unroll
+            for (int t = 0; t < ROWS; ++t) all |= __shfl(found, piece + t * PER, 64);
+            const uint32_t saw = m == -INFINITY ? 0u : ~0u;   // a row that saw nothing here counts for nothing in the joins
+            const float none = l == l ? 0.f : l;
 #pragma unroll
             for (int i = 0; i < A::OB; ++i)
 #pragma unroll
-                for (int e = 0; e < (int)(sizeof(acc) / 4); ++e) {
-                    const int at = (int)(sizeof(acc) / 4) * i + e;
-                    if (plus[at / 32] >> (at % 32) & 1u) o[i][e] += INFINITY;
-                    if (minus[at / 32] >> (at % 32) & 1u) o[i][e] -= INFINITY;
+                for (int q = 0; q < (int)(sizeof(acc) / 16); ++q) {
+                    const int d = R == 32 ? 32 * i + 8 * q + 4 * (lane >> 5) : 16 * i + 4 * (lane >> 4);
+                    const uint32_t bits = (uint32_t)__shfl(all, d >> 3, 64) >> (d & 4) & saw;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int at = (int)(sizeof(acc) / 4) * i + 4 * q + e;
+                        const bool up = (plus[at / 32] >> (at % 32) | bits >> e) & 1u, down = (minus[at / 32] >> (at % 32) | bits >> (8 + e)) & 1u;
+                        if (up || down) o[i][4 * q + e] = none + (up ? INFINITY : 0.f) - (down ? INFINITY : 0.f);
+                    }
                 }
         }
     }
 
     // join the slot groups of the workgroup, then write rows
-    l = row_sum<R>(l);
-    if (l != l) m = INFINITY;   // NaN among the logits: outweighs the other slot groups and chunks, whatever the maximum here
     const bool last = nchunk == 1;
     const int64_t prow = part_rows(b.rows, a.heads);
     float* const pout = (float*)a.work;
@@ -572,7 +620,7 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
         float M = -INFINITY;
 #pragma unroll
         for (int k = 0; k < KW; ++k) M = fmaxf(M, ml[(k * RW + rw) * R + lr].x);
-        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - M);
+        const float f = joined(m, M);
         float* mine = ol + ((kw * RW + rw) * R + lr) * A::OPAD;
         if constexpr (R == 32) {
 #pragma unroll
@@ -595,7 +643,7 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
 #pragma unroll
             for (int k = 0; k < KW; ++k) {
                 const float2 x = ml[k * RW * R + tr];
-                if (x.x != -INFINITY) lr_ += x.y * __builtin_amdgcn_exp2f(x.x - Mr);
+                if (x.x != -INFINITY) lr_ += x.y * joined(x.x, Mr);
             }
             f32x4 y = {0, 0, 0, 0};
 #pragma unroll
@@ -694,11 +742,11 @@ __global__ __launch_bounds__(256) void k_join_chunks(KvCache c, KvBatch b, AttnA
         for (int t = 32; t; t >>= 1) top = fmaxf(top, __shfl_xor(top, t, 64));
         const float Mn = fmaxf(M, top);
         if (Mn == -INFINITY) continue;   // nothing seen so far
-        const float f = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x.x - Mn);
+        const float f = joined(x.x, Mn);
         float ls = f == 0.f ? 0.f : x.y * f;
 #pragma unroll
         for (int t = 32; t; t >>= 1) ls += __shfl_xor(ls, t, 64);
-        const float keep = M == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(M - Mn);
+        const float keep = joined(M, Mn);
         l = l * keep + ls;
         y *= keep;
         M = Mn;
