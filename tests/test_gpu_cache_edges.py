@@ -1,7 +1,8 @@
 """GPU checks of the calls over the paged key/value cache at the edges of their
 definitions: weights far below one that dominates its row, evictions where the
 recent tokens alone exceed the budget, workspaces made for other sizes, steps without
-new tokens, infinities and NaN among the committed tokens.
+new tokens, infinities and NaN among the committed tokens,
+pages that are not there.
 
 Bounds as in test_gpu_cache.py: u is half an ulp of a type as a ratio, products
 and sums in fp32 add (D + 10) 2^-24 sum |q k| scale to a logit and n 2^-24 to a
@@ -352,3 +353,39 @@ def test_attention_of_infinite_values(bnn, T, heads, kv, dim, ctx, page, kind, o
         assert (np.abs(lse[i] - l) <= ds + (n + 8) * ref.E32 + 8 * ref.E32 * np.abs(l)).all()
         bound = u * np.where(odd, 0, A) + (2 * ds + 2 * n * ref.E32)[:, None] * np.where(odd, 0, A) + 2.0 ** -24
         assert (np.abs(got[i][~odd] - y[~odd]) <= bound[~odd]).all(), i
+
+
+# ---- pages that are not there
+
+@pytest.mark.parametrize("bad", [-1, 1 << 30])
+def test_evict_missing_pages(bnn, bad):
+    """A kept token whose page is not there reads as zeros, also once it has
+    moved; one that moves to a page that is not there is not written."""
+    banner(f"cache_evict missing page {bad}")
+    rng = np.random.default_rng(111)
+    n, kv, dim, keep = 96, 2, 64, 40
+    cache = ref.Paged(rng, 1, n, 16, kv, dim, BF)
+    for w in "KV":
+        cache.put(w, 0, np.arange(n), rng.standard_normal((n, kv, dim)))
+    cache.table[0, [1, 4]] = bad                  # slots 16-31 and 64-79
+    pos = np.stack([rng.permutation(n) for _ in range(kv)])[None].astype(np.int32)
+    score = rng.random((1, kv, n)).astype(np.float32)
+    dpos, dscore = torch.from_numpy(pos.copy()).cuda(), torch.from_numpy(score.copy()).cuda()
+    K, V = cache.K.clone(), cache.V.clone()
+    dc = cache.device(bnn, dpos, dscore)
+    bnn.cache_evict(dc, cuda_i32([0, 0]), cuda_i32([n]), budget=keep, recent=0, max_nodes=0, max_ctx=n)
+    torch.cuda.synchronize()
+    there = lambda s: s // 16 not in (1, 4)
+    moved_from_nowhere = 0
+    for h in range(kv):
+        source = evict_by_rank(n, np.zeros(0, dtype=bool), keep, 0, pos[0, h], score[0, h])
+        assert np.array_equal(dpos.cpu().numpy()[0, h, :keep], pos[0, h, source]) and np.array_equal(dscore.cpu().numpy()[0, h, :keep], score[0, h, source])
+        for to, come in enumerate(source):
+            if to != come and there(to):
+                moved_from_nowhere += not there(come)
+                for x in (K, V):
+                    page, at = cache.at(0, [to])
+                    x[page, at, h] = x[(*cache.at(0, [come]), h)] if there(come) else 0
+    assert moved_from_nowhere > 0
+    same = lambda x, y: torch.equal(x.contiguous().view(torch.int16), y.contiguous().view(torch.int16))
+    assert same(dc.k.cpu(), K) and same(dc.v.cpu(), V)

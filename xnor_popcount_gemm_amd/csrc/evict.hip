@@ -281,9 +281,12 @@ __global__ __launch_bounds__(256) void k_evict_move(KvCache c, EvictArgs a) {
         }
         uint32_t sp, dp;
         const int32_t spg = slot_page(c, seq, f, sp), dpg = slot_page(c, seq, t, dp);
-        if (spg < 0 || dpg < 0) continue;
-        const u32x4 k = *(const u32x4*)(c.K + spg * c.k_page + sp * c.k_slot + kh * c.k_head + u * 16);
-        const u32x4 v = *(const u32x4*)(c.V + spg * c.v_page + sp * c.v_slot + kh * c.v_head + u * 16);
+        if (dpg < 0) continue;
+        u32x4 k = {0, 0, 0, 0}, v = {0, 0, 0, 0};   // of a page that is not there
+        if (spg >= 0) {
+            k = *(const u32x4*)(c.K + spg * c.k_page + sp * c.k_slot + kh * c.k_head + u * 16);
+            v = *(const u32x4*)(c.V + spg * c.v_page + sp * c.v_slot + kh * c.v_head + u * 16);
+        }
         *(u32x4*)(c.K + dpg * c.k_page + dp * c.k_slot + kh * c.k_head + u * 16) = k;
         *(u32x4*)(c.V + dpg * c.v_page + dp * c.v_slot + kh * c.v_head + u * 16) = v;
     }
