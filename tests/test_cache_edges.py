@@ -80,3 +80,8 @@ def test_attention_workspace_covers_smaller_calls(bnn, sizes):
             for rows in {b * n, rng.randint(1, b * n)}:
                 need = workspace_bytes(bnn, b, rows, n, c, heads, kv, dim)
                 assert 0 <= need <= whole, (b, n, c, rows, need, whole)
+
+
+def test_attention_refuses_more_rows_than_it_counts(bnn):
+    assert workspace_bytes(bnn, 1, 1 << 25, 1 << 25, 10, 64, 1, 64) == -1       # 2^31 rows of one key head
+    assert workspace_bytes(bnn, 1, 1 << 24, 1 << 24, 10, 64, 1, 64) >= 0

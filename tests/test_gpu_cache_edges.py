@@ -2,7 +2,7 @@
 definitions: weights far below one that dominates its row, evictions where the
 recent tokens alone exceed the budget, workspaces made for other sizes, steps without
 new tokens, infinities and NaN among the committed tokens,
-pages that are not there.
+pages that are not there, launches of more than 2^24 workgroups.
 
 Bounds as in test_gpu_cache.py: u is half an ulp of a type as a ratio, products
 and sums in fp32 add (D + 10) 2^-24 sum |q k| scale to a logit and n 2^-24 to a
@@ -389,3 +389,55 @@ def test_evict_missing_pages(bnn, bad):
     assert moved_from_nowhere > 0
     same = lambda x, y: torch.equal(x.contiguous().view(torch.int16), y.contiguous().view(torch.int16))
     assert same(dc.k.cpu(), K) and same(dc.v.cpu(), V)
+
+
+# ---- more workgroups than one dimension of a launch takes
+
+def test_append_of_very_many_rows(bnn):
+    """2^24 + 3 new tokens, of which the cache has room for 16."""
+    banner("qk_norm_rope 2^24 + 3 rows")
+    rows = (1 << 24) + 3
+    q = torch.zeros((rows, 1, 64), dtype=BF, device="cuda")
+    q[-1], q[1 << 20], q[(1 << 20) - 1] = 1.0, 2.0, 3.0
+    k = torch.ones((1, 1, 64), dtype=BF, device="cuda").expand(rows, 1, 64)
+    K = torch.zeros((2, 16, 1, 64), dtype=BF, device="cuda")
+    cache = bnn.KVCache(K, torch.zeros_like(K))
+    out = torch.full_like(q, 7.0)
+    bnn.qk_norm_rope(q, k, k, cache, cuda_i32([0, rows - 1, rows]), cuda_i32([0, 5]), torch.zeros(rows, dtype=torch.int32, device="cuda"), None, q_out=out)
+    assert torch.equal(out, q)
+    want = torch.zeros_like(K)
+    want[0], want[1, 5] = 1, 1
+    assert torch.equal(K, want)
+
+
+def test_attention_of_very_many_workgroups(bnn):
+    """65535 sequences of 257 heads, one token each over one slot of a shared
+    page: each output is the slot's value of its head."""
+    banner("tree_attention 65535 x 257 workgroups")
+    B, heads = 65535, 257
+    K, V = torch.zeros((2, 2, heads, 64), dtype=BF, device="cuda"), torch.randn((2, 2, heads, 64), device="cuda").to(BF)
+    cache = bnn.KVCache(K, V, (torch.arange(B, dtype=torch.int32, device="cuda") % 2)[:, None].contiguous())
+    q = torch.zeros((1, heads, 64), dtype=BF, device="cuda").expand(B, heads, 64)
+    out, lse = bnn.tree_attention(q, cache, torch.arange(B + 1, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda"),
+                                  max_nodes=1, max_ctx=0)
+    assert torch.equal(out.view(torch.int16)[0::2], V[0, 0].view(torch.int16).expand(B - B // 2, -1, -1))
+    assert torch.equal(out.view(torch.int16)[1::2], V[1, 0].view(torch.int16).expand(B // 2, -1, -1)) and (lse == 0).all()
+
+
+def test_attention_join_of_very_many_rows(bnn):
+    """A token buffer of 2^24 + 3 rows whose sequences are cut into chunks."""
+    banner("tree_attention 2^24 + 3 rows, two chunks")
+    rows = (1 << 24) + 3
+    K, V = torch.zeros((2, 512, 1, 64), dtype=BF, device="cuda"), torch.randn((2, 512, 1, 64), device="cuda").to(BF)
+    cache = bnn.KVCache(K, V)
+    q = torch.zeros((1, 1, 64), dtype=BF, device="cuda").expand(rows, 1, 64)
+    out = torch.full((rows, 1, 64), 7.0, dtype=torch.float32, device="cuda")
+    work = torch.empty(2 * rows * (64 * 4 + 8), dtype=torch.uint8, device="cuda")
+    lse = torch.full((rows, 1), 7.0, device="cuda")
+    # all rows but two are the first sequence's; two tokens of each get an output
+    bnn.tree_attention(q, cache, cuda_i32([0, rows - 2, rows]), cuda_i32([300, 300]), max_nodes=2, max_ctx=300, out=out, lse=lse, workspace=work)
+    assert (out[2:-2] == 7).all() and (lse[2:-2] == 7).all()
+    for i, b, n in ((0, 0, 301), (1, 0, 302), (rows - 2, 1, 301), (rows - 1, 1, 302)):
+        # equal weights: the mean of n values of 8 bits, n roundings of a sum below 4 n, which is then divided by n
+        assert torch.allclose(out[i, 0], V[b, :n, 0].double().mean(0).float(), rtol=0, atol=4 * n * 2.0 ** -24)
+        assert abs(float(lse[i]) - np.log(n)) < 8 * 2.0 ** -24 * 6

@@ -51,7 +51,8 @@ AttnPlan make_plan(const KvCache& c, const KvBatch& b, int32_t heads, int64_t wo
     p.chunks = (int32_t)((slots + chunk - 1) / chunk);
     if (p.chunks < 1) p.chunks = 1;
     const int64_t groups = (int64_t)b.B * kv_heads * p.chunks;
-    p.groups = groups < 0x7FFFFFFF / 16 && (groups + 8) * tiles < 0x7FFFFFFF ? (int32_t)groups : -1;   // -1: past one launch
+    // -1: more rows or workgroups than the kernel counts
+    p.groups = rows < 0x7FFFFFFF - tile && groups < 0x7FFFFFFF / 16 && (groups + 8) * tiles < 0x7FFFFFFF ? (int32_t)groups : -1;
     return p;
 }
 

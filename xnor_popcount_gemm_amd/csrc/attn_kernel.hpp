@@ -204,7 +204,7 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
     const int rw = wave % RW, kw = wave / RW;
     // Workgroups go to the 8 XCDs in turn, and each XCD has its own L2: the row tiles of a chunk of a key head,
     // which read the same K and V, take every eighth place.
-    const uint32_t idx = blockIdx.x / 8, group = idx / pl.row_tiles * 8 + blockIdx.x % 8;
+    const uint32_t block = wide_index(blockIdx.y), idx = block / 8, group = idx / pl.row_tiles * 8 + block % 8;
     if (group >= (uint32_t)pl.groups) return;
     const int rt = idx % pl.row_tiles, ci = group % pl.chunks, pair = group / pl.chunks, kh = pair % c.kv_heads, seq = pair / c.kv_heads;
 
@@ -707,9 +707,9 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
 template <int D, typename O, bool AHEAD>
 __global__ __launch_bounds__(256) void k_join_chunks(KvCache c, KvBatch b, AttnArgs a, AttnPlan pl) {
     constexpr int PER = D / 4, PARTS = 64 / PER, EARLY = 16;
-    const int row = blockIdx.x, lane = threadIdx.x & 63;
+    const int row = wide_index(blockIdx.z), lane = threadIdx.x & 63;
     const int h = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (h >= a.heads) return;
+    if (row >= b.rows || h >= a.heads) return;
     const int64_t prow = part_rows(b.rows, a.heads), at = (int64_t)row * a.heads + h;
     const float* const pout = (const float*)a.work + at * D;
     const float2* const pml = (const float2*)(a.work + (int64_t)pl.chunks * prow * D * 4) + at;
@@ -784,7 +784,8 @@ __global__ __launch_bounds__(256) void k_join_chunks(KvCache c, KvBatch b, AttnA
 
 template <typename T, int D, int R, int RW, int KW, int NS, typename O>
 void launch_tiles(const KvCache& c, const KvBatch& b, const AttnArgs& a, const AttnPlan& pl, hipStream_t s) {
-    const dim3 grid((unsigned)(((int64_t)pl.groups + 7) / 8 * 8 * pl.row_tiles));
+    const int64_t blocks = ((int64_t)pl.groups + 7) / 8 * 8 * pl.row_tiles;
+    const dim3 grid(wide(blocks), parts(blocks));
     hipLaunchKernelGGL((k_tree_attention<T, D, R, RW, KW, NS, O>), grid, dim3(RW * KW * 64), 0, s, c, b, a, pl);
 }
 
@@ -797,7 +798,7 @@ hipError_t launch_dim(const KvCache& c, const KvBatch& b, const AttnArgs& a, con
     else launch_tiles<T, D, 32, 4, 1, NS, O>(c, b, a, pl, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || pl.chunks == 1) return e;
-    const dim3 grid(b.rows, (a.heads + 3) / 4);
+    const dim3 grid(wide(b.rows), (a.heads + 3) / 4, parts(b.rows));
     if ((int64_t)b.rows * a.heads <= 2048) hipLaunchKernelGGL((k_join_chunks<D, O, true>), grid, dim3(256), 0, s, c, b, a, pl);
     else hipLaunchKernelGGL((k_join_chunks<D, O, false>), grid, dim3(256), 0, s, c, b, a, pl);
     return hipGetLastError();

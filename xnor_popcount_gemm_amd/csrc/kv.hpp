@@ -97,6 +97,13 @@ __device__ __forceinline__ bool packed_bit(const uint32_t* row, int64_t words, i
     return (i >> 5) < words && ((row[i >> 5] >> (i & 31)) & 1u);
 }
 
+// A launch takes fewer than 2^32 threads along a dimension; more than 2^20
+// workgroups go on in a second one, `part`.
+constexpr int64_t WIDE = (int64_t)1 << 20;
+inline unsigned wide(int64_t groups) { return (unsigned)(groups < WIDE ? groups : WIDE); }
+inline unsigned parts(int64_t groups) { return (unsigned)((groups + WIDE - 1) / WIDE); }
+__device__ __forceinline__ uint32_t wide_index(uint32_t part) { return part * (uint32_t)WIDE + blockIdx.x; }
+
 // A row of zeros, read in place of a row that is not there.
 namespace {
 __device__ __align__(64) const uint32_t zero_row[128] = {};

@@ -35,7 +35,8 @@ template <typename T, typename S, int LPR, bool INTER>
 __global__ __launch_bounds__(256) void k_qk_norm_rope(KvCache c, KvBatch b, RopeArgs a) {
     constexpr int ESZ = sizeof(S) == 4 ? 4 : 2;
     constexpr int HEADS = 256 / LPR;   // heads in flight per workgroup
-    const int row = blockIdx.x, tid = threadIdx.x;
+    const int row = wide_index(blockIdx.y), tid = threadIdx.x;
+    if (row >= b.rows) return;
     const int seq = row_sequence(b, row, tid & 63);
     if (seq < 0) return;
     const Seq sq = sequence(c, b, seq);
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(KvCache c, KvBatch b, Rope
 
 template <typename T, typename S, int LPR>
 void launch_one(const KvCache& c, const KvBatch& b, const RopeArgs& a, bool inter, hipStream_t s) {
-    const dim3 grid(b.rows);
+    const dim3 grid(wide(b.rows), parts(b.rows));
     if (inter) hipLaunchKernelGGL((k_qk_norm_rope<T, S, LPR, true>), grid, dim3(256), 0, s, c, b, a);
     else       hipLaunchKernelGGL((k_qk_norm_rope<T, S, LPR, false>), grid, dim3(256), 0, s, c, b, a);
 }
