@@ -51,7 +51,8 @@ __device__ __forceinline__ float over_rows(float s0, float s1) {
 // of a run and its masked tiles (so that no wave gets many short sequences one
 // after the other); nothing where nothing is to be added.
 constexpr int START = 3;
-__device__ __forceinline__ int cost_of(const KvCache& c, const KvBatch& b, int s) {
+static_assert(64 * (((int64_t)1 << 30) / 32 + START) < (int64_t)1 << 32, "the costs of 64 sequences of 2^30 slots are added in 32 bits");
+__device__ __forceinline__ uint32_t cost_of(const KvCache& c, const KvBatch& b, int s) {
     const Seq q = sequence(c, b, s);
     return q.nodes ? (q.total + 31) / 32 + START : 0;
 }
@@ -84,35 +85,35 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_cache_score_add(KvCac
 
     // this wave's share of the cost, in the order sequence, key head, tile; 64 sequences per step
     int64_t all = 0;
-    int cost0 = 0, upto0 = 0;   // of sequence `lane`: its cost, and that of the sequences up to it
+    uint32_t cost0 = 0, upto0 = 0;   // of sequence `lane`: its cost, and that of the sequences up to it
     for (int s0 = 0; s0 < b.B; s0 += 64) {
-        const int n = s0 + lane < b.B ? cost_of(c, b, s0 + lane) : 0;
-        int upto = n;
+        const uint32_t n = s0 + lane < b.B ? cost_of(c, b, s0 + lane) : 0;
+        uint32_t upto = n;
 #pragma unroll
-        for (int m = 1; m < 64; m <<= 1) { const int x = __shfl_up(upto, m, 64); upto += lane >= m ? x : 0; }
+        for (int m = 1; m < 64; m <<= 1) { const uint32_t x = __shfl_up(upto, m, 64); upto += lane >= m ? x : 0; }
         if (s0 == 0) { cost0 = n; upto0 = upto; }
-        all += __builtin_amdgcn_readlane(upto, 63);   // below 2^31: 64 sequences of 2^25 tiles at most
+        all += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
     }
     all *= c.kv_heads;
     int64_t left = all * (me + 1) / waves - all * me / waves, skip = all * me / waves;
     int seq = 0, mine = 0;   // the sequence of the first unit, and its cost
     if (left > 0)
         for (int s0 = 0;; s0 += 64) {
-            int n = cost0, upto = upto0;
+            uint32_t n = cost0, upto = upto0;
             if (s0 > 0) {
                 n = s0 + lane < b.B ? cost_of(c, b, s0 + lane) : 0;
                 upto = n;
 #pragma unroll
-                for (int m = 1; m < 64; m <<= 1) { const int x = __shfl_up(upto, m, 64); upto += lane >= m ? x : 0; }
+                for (int m = 1; m < 64; m <<= 1) { const uint32_t x = __shfl_up(upto, m, 64); upto += lane >= m ? x : 0; }
             }
             const int before = __popcll(__ballot((int64_t)upto * c.kv_heads <= skip));   // whole sequences skipped
             if (before < 64) {
                 seq = s0 + before;
                 mine = __builtin_amdgcn_readlane(n, before);
-                skip -= (int64_t)(__builtin_amdgcn_readlane(upto, before) - mine) * c.kv_heads;
+                skip -= (int64_t)((uint32_t)__builtin_amdgcn_readlane(upto, before) - (uint32_t)mine) * c.kv_heads;
                 break;
             }
-            skip -= (int64_t)__builtin_amdgcn_readlane(upto, 63) * c.kv_heads;
+            skip -= (int64_t)(uint32_t)__builtin_amdgcn_readlane(upto, 63) * c.kv_heads;
         }
     int kh = left > 0 ? (int)(skip / mine) : 0, unit = left > 0 ? (int)(skip % mine) : 0;
 
