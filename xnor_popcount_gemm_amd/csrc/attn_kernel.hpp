@@ -20,8 +20,10 @@
 // all; float16 ones end at 2^-24, and slots far below one that dominates the
 // row (whose V may be near 0) would be lost.  There the reference follows each
 // step's maximum both ways, so that the step's largest weight lies in
-// 2^5 .. 2^15 (2^12 where it is moved, at most 2^48 below its peak): a weight is
-// then off by its rounding or by 2^-30 of the largest of its 32 or 64 slots.
+// 2^5 .. 2^15.5 (2^10 where it is moved, at most 2^48 below its peak): a weight
+// is then off by its rounding or by 2^-30 of the largest of its 32 or 64 slots.
+// Trees of 63 tokens over 32000 slots take 198 us that way (193 without, 201
+// where it is moved to 2^12: some row of a wave does so at most steps).
 //
 // Tiles.  K and V rows go from global memory straight to LDS (16 bytes per
 // lane); the next step's rows are in flight while one is worked on, in a
@@ -169,7 +171,7 @@ struct Attn {
 
     // base-2 logarithms of a float16 step's largest weight: bounds, where it is put, and how far the reference may sink
     static constexpr bool NARROW = std::is_same<T, F16>::value;
-    static constexpr float HIGH = NARROW ? 15.f : 8.f, LOW = 5.f, AIM = 12.f, DEEP = 48.f;
+    static constexpr float HIGH = NARROW ? 15.5f : 8.f, LOW = 5.f, AIM = 10.f, DEEP = 48.f;
 
     static constexpr int PW = (OB * (int)sizeof(acc) / 4 + 31) / 32;   // words of a bit per accumulator
 
@@ -312,7 +314,7 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
 #pragma unroll
     for (int i = 0; i < A::OB; ++i) o[i] = acc{};
     float m = -INFINITY, l = 0.f;   // reference (base-2 logarithm) and this lane's share of the sum
-    float peak = -INFINITY;         // the highest reference so far
+    float peak = -INFINITY, least = A::LOW;   // the highest reference so far; what lowers it
     // which of this lane's dimensions saw +inf / -inf: bit 4 i + e of dimension e of its piece i of 4
     uint32_t plus[A::PW], minus[A::PW];
 #pragma unroll
@@ -388,17 +390,17 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
 #pragma unroll
             for (int i = 0; i < A::NSC; ++i) mx = fmaxf(mx, sc[sub][i]);
         mx = row_max<R>(mx) * c2;
-        bool move = mx > m + A::HIGH;
-        float mn = fmaxf(m, mx);
-        if constexpr (A::NARROW) {
-            const float want = fmaxf(mx - A::AIM, peak - A::DEEP);
-            move = move || (mx > -INFINITY && want < m - (A::AIM - A::LOW));
-            mn = move ? want : m;
-        }
-        if (__any(move)) {
+        const float over = mx - m;
+        if (__any(over > A::HIGH || (A::NARROW && over < least))) {
+            float mn = fmaxf(m, mx);
+            if constexpr (A::NARROW) {
+                mn = m;
+                if (mx > -INFINITY && (over > A::HIGH || over < least)) mn = fmaxf(mx - A::AIM, peak - A::DEEP);
+                peak = fmaxf(peak, mn);
+                least = mn > peak - A::DEEP ? A::LOW : -INFINITY;
+            }
             const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
             m = mn;
-            if (A::NARROW) peak = fmaxf(peak, m);
             l *= f;
 #pragma unroll
             for (int i = 0; i < A::OB; ++i) o[i] *= f;
