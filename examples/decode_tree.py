@@ -87,6 +87,14 @@ def draft(rng: random.Random, nodes: int):
     return parents, path[::-1]
 
 
+def packed(path, nodes: int):
+    """A set of nodes as signed 32-bit words, bit i % 32 of word i / 32 for node i."""
+    words = [0] * ((nodes + 31) // 32)
+    for i in path:
+        words[i // 32] |= 1 << (i % 32)
+    return [w - (1 << 32) if w >> 31 else w for w in words]
+
+
 def run(steps: int = 40, sequences: int = 4, seed: int = 0, **kw):
     """Decodes; returns the block, the last outputs and each sequence's length."""
     block = Block(sequences, seed=seed, **kw)
@@ -101,7 +109,7 @@ def run(steps: int = 40, sequences: int = 4, seed: int = 0, **kw):
                 d[i] = d[p] + 1 if p >= 0 else 0
         mask = torch.cat([bnn.tree_mask(parents) for parents, _ in trees]).cuda()
         positions = torch.tensor([n + x for n, d in zip(length, depth) for x in d], dtype=torch.int32).cuda()
-        bits = torch.tensor([[sum(1 << i for i in path)] for _, path in trees], dtype=torch.int64).to(torch.int32).cuda()
+        bits = torch.tensor([packed(path, block.nodes) for _, path in trees], dtype=torch.int32).cuda()
         x = torch.randn((sequences * block.nodes, block.qkv.K), generator=g, device="cuda")
         y, seen = block.attend(x, indptr, positions, mask)
         block.accept(seen, bits)

@@ -2,7 +2,8 @@
 definitions: weights far below one that dominates its row, evictions where the
 recent tokens alone exceed the budget, workspaces made for other sizes, steps without
 new tokens, infinities and NaN among the committed tokens,
-pages that are not there, launches of more than 2^24 workgroups.
+pages that are not there, launches of more than 2^24 workgroups, trees of more
+nodes than a word has bits.
 
 Bounds as in test_gpu_cache.py: u is half an ulp of a type as a ratio, products
 and sums in fp32 add (D + 10) 2^-24 sum |q k| scale to a logit and n 2^-24 to a
@@ -441,3 +442,21 @@ def test_attention_join_of_very_many_rows(bnn):
         # equal weights: the mean of n values of 8 bits, n roundings of a sum below 4 n, which is then divided by n
         assert torch.allclose(out[i, 0], V[b, :n, 0].double().mean(0).float(), rtol=0, atol=4 * n * 2.0 ** -24)
         assert abs(float(lse[i]) - np.log(n)) < 8 * 2.0 ** -24 * 6
+
+
+# ---- trees of more nodes than a word has bits
+
+def test_example_of_wide_trees(bnn):
+    """The example's path with 70 drafts: while the budget lasts the cache holds
+    every accepted token."""
+    banner("examples/decode_tree.py, 70 nodes")
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import decode_tree
+    block, y, length = decode_tree.run(steps=8, sequences=3, hidden=256, heads=4, kv_heads=2, dim=64, budget=400, recent=16, nodes=70)
+    torch.cuda.synchronize()
+    assert y.isfinite().all() and max(length) < 400 and block.ctx.tolist() == length
+    for b in range(3):
+        for h in range(2):
+            assert sorted(block.cache.pos[b, h, : length[b]].tolist()) == list(range(length[b]))
