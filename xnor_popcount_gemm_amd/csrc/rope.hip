@@ -36,9 +36,8 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(KvCache c, KvBatch b, Rope
     constexpr int ESZ = sizeof(S) == 4 ? 4 : 2;
     constexpr int HEADS = 256 / LPR;   // heads in flight per workgroup
     const int row = wide_index(blockIdx.y), tid = threadIdx.x;
-    if (row >= b.rows) return;
     const int seq = row_sequence(b, row, tid & 63);
-    if (seq < 0) return;
+    if (seq < 0 || row >= b.rows) return;
     const Seq sq = sequence(c, b, seq);
     const int64_t slot = (int64_t)sq.ctx + (row - sq.row0);
     const bool fits = slot < sq.total;
