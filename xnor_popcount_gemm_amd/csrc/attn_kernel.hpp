@@ -537,7 +537,10 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
     } else {
         auto next = [&](int st) {   // step st is in LDS; the next one is on its way
             wait_all();
-            if (RW > 1) __builtin_amdgcn_s_barrier();
+            if (RW > 1) {
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");   // no read of the tile moves up over the barrier
+            }
             if (st + 1 < steps) {
                 fetch((st + 1) & 1);
                 if (st + 2 < steps) lookup(st + 2, k1);
