@@ -5,13 +5,18 @@
 // The rows of a (sequence, key head) are its new tokens times the query heads
 // that share the key head, so one pass over K and V serves them all.
 //
-// Products.  Scores are computed transposed, S^T = K Q^T: a lane then holds
-// one row's scores for 8 or 16 of a step's 32 slots, so the softmax
-// statistics are a few in-lane operations and one or two lane swaps, and the
-// weights are already laid out as the second operand of O^T = V^T P^T: no
-// weight crosses a lane.  What V^T needs is a transposed read of V's rows,
-// which ds_read_b64_tr_b16 gives.  R = 16 rows per wave use 16x16x32 matrix
-// instructions, R = 32 rows 32x32x16.
+// Products.  Scores are computed transposed, S^T = K Q^T: a lane then holds one
+// row's scores for 8 or 16 of a step's 32 slots, so the softmax statistics are
+// a few in-lane operations and one or two lane swaps, and the weights are
+// already laid out as the second operand of O^T = V^T P^T: no weight crosses a
+// lane.  That operand has the cache's 16 bits.  With a 16-bit output a weight
+// is rounded once to it, by half an ulp like the output itself (errors against
+// 64 bits a third larger than with exact weights, 0.0023 for 0.0017); with fp32
+// output it is split into the terms that keep it, two of float16 or three of
+// bfloat16, each a product more: 1024 tokens over 8192 take 291 us instead of
+// 183, in float16 246 instead of 192.  What V^T needs is a transposed read of
+// V's rows, which ds_read_b64_tr_b16 gives.  R = 16 rows per wave use 16x16x32
+// matrix instructions, R = 32 rows 32x32x16.
 //
 // Running maximum.  Weights are taken relative to a reference that is only
 // raised when a score passes it by more than 2^8 (in the base-2 logarithm):
@@ -29,34 +34,37 @@
 // lane); the next step's rows are in flight while one is worked on, in a
 // second buffer where the waves of a workgroup share the tile.  With up to 32
 // rows each wave has tiles of its own, which pass on to registers so that one
-// buffer will do and twice the waves fit a compute unit.  A wave's load brings 1 KiB: 8 rows of 128 bytes, whole cache lines
-// (16 rows of 64 bytes for 96 dimensions).  Where one row tile reads them,
-// without keeping them in the caches: 64 sequences of about 6200 slots take
-// 285 us by whole lines that way (5.6 TB/s) and 311 kept; in half lines 396
-// and 327.  The 16-byte pieces of row r are
-// permuted by XOR so that the lanes served together read different banks: by
-// r % 8 for K (b128 reads of one piece of 8 slots), by 2 (r % 4) for V
-// (transposed reads of two pieces of 4 slots).  Rows past the end are read
-// from a block of zeros.
+// buffer will do and twice the waves fit a compute unit.  A wave's load brings
+// 1 KiB.  With up to 32 rows that is 8 rows of 128 bytes, whole cache lines (16
+// rows of 64 for 96 dimensions), read without keeping them in the caches: 64
+// sequences of about 6200 slots take 285 us that way (5.6 TB/s) and 311 kept; in
+// half lines 396 and 327.  With more rows the row tiles share the caches, and a
+// load brings 16 rows of 64 bytes, which halves a lane's page lookups.  The
+// 16-byte pieces of row r are permuted by XOR so that the lanes served together
+// read different banks: of 128-byte rows by r % 8 for K (b128 reads of one piece
+// of 8 slots) and by 2 (r % 4) for V (transposed reads of two pieces of 4 slots),
+// of 64-byte rows by (r / 2) % 4 and 2 ((r / 2) % 2), which leaves a third of the
+// LDS cycles to conflicts.  Rows past the end are read from a block of zeros.
 //
 // Masks.  Committed slots are seen by every row and cost nothing, and so do the
-// new tokens of a causal run up to the first row's own (a prompt of 4096 tokens:
-// 182 us; 212 with these steps among the masked ones).  Steps that hold other
-// new tokens take one 32-bit word per row and 32 slots, and run as the others do
-// where every row sees them whole.  An unseen token must not matter even where
-// its V is NaN or infinite, and 0 * NaN is NaN, so a masked step takes such values as 0 in
-// the products and notes, as bits per row and dimension, which rows saw an
-// infinity of which sign (NaN: both); the infinities are added at the end.  A
-// plain step has no such care: a weight that was rounded to 0, or the negative
-// remainder of one, makes NaN of a committed infinity.  Where a wave's result is
-// not finite it reads V of the slots that all rows see once more for what they
-// hold.
+// new tokens of a causal run up to the first row's own (a prompt of 4096
+// tokens: 182 us; 212 with these steps among the masked ones).  Steps that hold
+// other new tokens take one 32-bit word per row and 32 slots, and run as the
+// others do where every row sees them whole.  An unseen token must not matter
+// even where its V is NaN or infinite, and 0 * NaN is NaN, so a masked step
+// takes such values as 0 in the products and notes, as bits per row and
+// dimension, which rows saw an infinity of which sign (NaN: both); the
+// infinities are added at the end.  A plain step has no such care: a weight
+// that was rounded to 0, or the negative remainder of one, makes NaN of a
+// committed infinity.  Where a wave's result is not finite it reads V of the
+// slots that all rows see once more for what they hold.
+//
 // What bounds it.  Few rows: the read of K and V; 285 us for 1.59 GB, where the
 // same paged rows fetched and not used take about 265.  Many rows: neither the
-// matrix cores (busy 39% of the time at a 1024-token chunk, 790 TFLOP/s) nor
-// the vector unit (32%) nor LDS (30%) is full: two waves per SIMD wait for each
-// other's products, exponentials and the shared tile in turn; without any
-// fetch the same steps reach 990 TFLOP/s.
+// matrix cores (busy 41% of the time at a 1024-token chunk, 830 TFLOP/s) nor
+// the vector unit (33%) nor LDS (31%) is full: two waves per SIMD wait for each
+// other's products, exponentials and the shared tile in turn; without the
+// fetches the same steps reach 940, those of trees 980 instead of 755.
 #pragma once
 
 #include <math.h>
@@ -420,7 +428,7 @@ __global__ __launch_bounds__(RW * KW * 64, (D == 256 ? 1 : 2)) void k_tree_atten
 
 #pragma unroll
         for (int sub = 0; sub < A::SUB; ++sub) {
-            // weights as 16-bit operands: one term, or as many as keep them whole
+            // weights as 16-bit operands: one term where the output is rounded as much, or as many as keep them whole
             vec8 pf[A::NSC / 8][NS];
 #pragma unroll
             for (int g = 0; g < A::NSC / 8; ++g) {

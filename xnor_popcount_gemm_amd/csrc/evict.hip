@@ -19,7 +19,7 @@
 // a second kernel moves K and V rows (and positions and scores) in any order.
 // It is bound by memory: 117 MB of reads and writes in 30 us, 3.9 TB/s, where a
 // plain copy reaches 5.1.  The first kernel is bound by its passes in one
-// workgroup per head: 13 us at 2048 slots, 51 at 32000.
+// workgroup per head: 13 us at 2048 slots, 50 at 32000.
 #include <math.h>
 
 #include "bnn_device.hpp"

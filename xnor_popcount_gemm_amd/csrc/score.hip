@@ -9,8 +9,11 @@
 // as the second operand of S = Q K^T in 16x16x32 matrix products, and the next
 // 32 rows are on their way to the same LDS while these are worked on.  Up to
 // 32 accepted rows (new tokens times query heads of the group) stay in LDS
-// over all slots; more pass by in batches of 32.  Nothing but K is waited for
-// in the loop: a load behind the next K rows would hold their whole latency.
+// over all slots, and nothing but K is waited for in the loop: a load behind the
+// next K rows would hold their whole latency.  More rows, and those of more than
+// 64 new tokens, pass by in batches of 32 at each tile, each waited for with the
+// next K rows: that is bound by these waits (the case below with 36 rows 116 us
+// instead of 76, a chunk of 1024 tokens over 8192 424 us).
 // A lane holds one slot's products with 4 rows, so the sum over rows runs in
 // registers and two lane swaps finish it; no atomics, a fixed order.
 //
