@@ -636,6 +636,174 @@ bnn_status bnn_cache_evict(const bnn_kv_cache* cache, const bnn_kv_batch* batch,
  * arguments that it would refuse. */
 int64_t bnn_cache_evict_workspace(const bnn_kv_cache* cache, int64_t B);
 
+/* ----------------------------------------------------------------------
+ * The decoder's feed-forward half.
+ *
+ * What runs between the attention's output projection and the next block's
+ * first projection, where the linear layers are 1-bit ones on INT8 rows
+ * ([P5] "BitNet: 1-bit Transformer"; [P3]: norms and the residual stream stay
+ * at higher precision):
+ *   bnn_block_norm     experts' outputs joined, norm, gate, residual, norm,
+ *                      INT8 quantization, in one pass
+ *   bnn_expert_route   each token's experts, and the tokens sorted by expert
+ *   bnn_expert_linear  binary or ternary matrices x INT8 rows, by expert, with
+ *                      bias, activation, gate and residual in the epilogue
+ * Which expert has how many rows is read from device memory, so a step of
+ * them can be captured in a HIP graph.
+ * ---------------------------------------------------------------------- */
+#define BNN_NORM_NONE  0
+#define BNN_NORM_RMS   1   /* v / sqrt(mean(v^2) + eps) * weight (+ bias)             */
+#define BNN_NORM_LAYER 2   /* the same of v - mean(v)                                 */
+
+/* Longest row of bnn_block_norm. */
+#define BNN_MAX_NORM_D ((int64_t)16384)
+
+/* Arguments of bnn_block_norm.  Host struct, device pointers.  The types are
+ * BNN_F32, BNN_BF16 or BNN_F16.  Rows need only the alignment of their type;
+ * they are read and written 4 values at a time where the address is a multiple
+ * of 4 values and the stride of 4 (of 16 bytes for Xq). */
+typedef struct bnn_norm_args {
+    int64_t M, D;                             /* rows; 1 <= D <= BNN_MAX_NORM_D  */
+    const int32_t* used;                      /* [1]: rows used[0] .. M-1 are neither read
+                                                 nor written.  NULL: all M        */
+    const void* x; int64_t ldx; int32_t x_dtype;       /* [M, ldx], the residual stream, or NULL */
+    const void* branch; int64_t ldb; int32_t b_dtype;  /* [b_rows, ldb], or NULL; x or branch must be there */
+    int64_t b_rows;                           /* rows of branch (at least M without place) */
+    const int32_t* place; const float* weight;/* [M, parts]: the rows of branch that make row m,
+                                                 and their weights (NULL: 1).  NULL: row m */
+    int64_t parts;                            /* 1 .. 64, with place             */
+    int32_t post;                             /* norm of the branch               */
+    const float* post_weight; const float* post_bias;  /* [D] or NULL             */
+    const float* gate; int64_t ld_gate;       /* [D] with ld_gate 0, [M, ld_gate], or NULL */
+    float x_scale, branch_scale;
+    int32_t pre;                              /* norm of the stream               */
+    const float* pre_weight; const float* pre_bias;    /* [D] or NULL             */
+    float eps;
+    void* x_out; int64_t ldxo;                /* [M, ldxo] in x_dtype, or NULL; may be x   */
+    void* y; int64_t ldy; int32_t y_dtype;    /* [M, ldy] or NULL                 */
+    int8_t* Xq; int64_t ldXq;                 /* as in bnn_quantize_act_i8; any of Xq, Xb may */
+    uint32_t* Xb; int64_t ldXb;               /* be NULL, xsum is needed with Xb, xscale with */
+    int32_t* xsum; float* xscale;             /* either                           */
+} bnn_norm_args;
+
+/* For every row, in one pass:
+ *     b  = sum_j weight[m,j] branch[place[m,j]]     (place NULL: branch[m]; places
+ *                                                     outside the branch add nothing)
+ *     s  = x_scale x[m] + branch_scale gate . post(b)
+ *     x_out[m] = s;    y = pre(s);    Y[m] = y
+ *     Xq[m], Xb[m], xsum[m], xscale[m] = INT8 rows of y as bnn_quantize_act_i8
+ *                                        lays them out, with inv = fl32(127
+ *                                        fl32(1 / amax)): a code next to a
+ *                                        border may be the neighbouring one
+ * Everything up to y is computed in 64 bits, s is rounded to x's type where
+ * x_out is given (pre then reads the rounded stream, as a call of its own on
+ * x_out would) and y to fp32; 16-bit outputs are rounded from fp32.  The
+ * 64 bits cost nothing beside the memory traffic and make codes and scales the
+ * same whatever the order of the sums.  A row's norms are over its D values;
+ * without x or branch their term is left out.  At least one output must be
+ * given. */
+bnn_status bnn_block_norm(const bnn_norm_args* args, bnn_stream_t stream);
+
+#define BNN_ROUTE_SOFTMAX 0   /* score = softmax of the row's logits */
+#define BNN_ROUTE_SIGMOID 1   /* score = 1 / (1 + exp(-logit))       */
+#define BNN_MAX_EXPERTS ((int64_t)1024)
+
+/* Arguments of bnn_expert_route.  Host struct, device pointers. */
+typedef struct bnn_route_args {
+    const void* logits; int64_t ld;           /* [rows, ld >= experts]            */
+    int32_t dtype;                            /* BNN_F32, BNN_BF16 or BNN_F16     */
+    int64_t rows, experts, top;               /* experts 1 .. BNN_MAX_EXPERTS; top 1 .. min(experts, 64);
+                                                 rows * top < 2^30                */
+    const int32_t* used;                      /* [1]: rows from used[0] on get no expert, and
+                                                 their outputs are left alone.  NULL: all rows */
+    int32_t score;                            /* BNN_ROUTE_*                      */
+    const float* bias;                        /* [experts] or NULL                */
+    int32_t renorm; float scale;
+    int32_t* expert; float* weight;           /* [rows, top]                      */
+    int32_t* offsets;                         /* [experts + 1]                    */
+    int32_t* order;                           /* [rows * top]                     */
+    int32_t* place;                           /* [rows, top]                      */
+    void* workspace; int64_t workspace_bytes; /* bnn_expert_route_workspace bytes, 16-byte aligned */
+} bnn_route_args;
+
+/* The experts of every row: the `top` of the largest logits, or with bias of
+ * the largest score + bias (in 64 bits, so that near ties do not depend on
+ * rounding); equal ones by the lowest index, in descending order.  An expert
+ * whose logit (or score + bias) is -inf or NaN is never chosen: a row with
+ * fewer than `top` others has -1 as its last experts, with weight 0 and place
+ * -1.  weight = score, divided by the sum over the row's chosen ones with
+ * renorm (a sum of 0 gives weights 0), times scale, in fp32.  In a softmax NaN
+ * logits count as -inf and one of +inf makes the row's weights NaN.
+ * The pairs (row, choice) of an expert, in order of row * top + choice, take
+ * the positions offsets[e] .. offsets[e+1]-1: order[position] = row * top +
+ * choice and place[row, choice] = position.  Entries of order from
+ * offsets[experts] on are left alone. */
+bnn_status bnn_expert_route(const bnn_route_args* args, bnn_stream_t stream);
+
+/* Workspace bytes of bnn_expert_route (0 where it uses none); -1 for sizes
+ * that it would refuse. */
+int64_t bnn_expert_route_workspace(int64_t rows, int64_t experts, int64_t top);
+
+/* Weights as bnn_expert_linear reads them, laid out once from the packed
+ * planes of bnn_pack_weights (Zp NULL: 1 bit a weight) or
+ * bnn_pack_weights_ternary (2 bits).  The planes are [experts, N, ldWp], those
+ * of two experts w_expert words apart.  out: bnn_expert_pack_bytes bytes,
+ * 16-byte aligned.  Layout: 16 rows by 64 k are a fragment of the matrix
+ * cores, lane l of it row l % 16 and k = 16 (l / 16) + 4 d + j, d, j < 4; a
+ * lane holds 16 bytes, 4 fragments of ternary weights (a word each, codes 0, 1
+ * and 3 = -1 at bits 8 j + 2 d) or 8 of binary ones (two to a word, d + 4 for
+ * the second, 1 = -1 at bits 8 j + d); 64 lanes make 1 KiB, in the order
+ * [expert, N / 16, K / 256 or 512].  Rows past N and k past K hold 0. */
+bnn_status bnn_expert_pack(const uint32_t* Wp, const uint32_t* Zp, int64_t ldWp, int64_t w_expert,
+                           int64_t experts, int64_t N, int64_t K, void* out, int64_t out_bytes, bnn_stream_t stream);
+
+/* Bytes of the above; -1 for sizes that it would refuse. */
+int64_t bnn_expert_pack_bytes(int64_t experts, int64_t N, int64_t K, int32_t ternary);
+
+/* Activations of bnn_expert_linear. */
+#define BNN_ACT_NONE      0
+#define BNN_ACT_RELU      1
+#define BNN_ACT_RELU2     2   /* max(z, 0)^2                                      */
+#define BNN_ACT_SILU      3   /* z / (1 + exp(-z))                                */
+#define BNN_ACT_GELU      4   /* z Phi(z)                                         */
+#define BNN_ACT_GELU_TANH 5   /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2  */
+
+/* A matrix of bnn_expert_linear.  Device pointers. */
+typedef struct bnn_expert_matrix {
+    const void* W;                            /* bnn_expert_pack                  */
+    const float* alpha; int64_t ld_alpha;     /* [experts, ld_alpha >= N]; ld_alpha 0: one scale
+                                                 for each expert, alpha[experts]  */
+    const float* bias; int64_t ld_bias;       /* [experts, ld_bias >= N], or NULL */
+} bnn_expert_matrix;
+
+/* Arguments of bnn_expert_linear.  Host struct, device pointers. */
+typedef struct bnn_expert_args {
+    const int8_t* Xq; int64_t ldXq;           /* [rows, ldXq]: 16-byte aligned, ldXq a multiple of
+                                                 16 and >= K; bytes from K on are ignored */
+    const float* xscale;                      /* [rows], or NULL: 1               */
+    int64_t rows;
+    const int32_t* order; int64_t per_row;    /* position p reads row order[p] / per_row; NULL:
+                                                 row p (rows >= positions)        */
+    const int32_t* offsets;                   /* [experts + 1]: expert e has the positions
+                                                 offsets[e] .. offsets[e+1]-1; they must not
+                                                 decrease.  NULL (experts 1): all */
+    int64_t experts, positions, N, K;         /* K <= BNN_MAX_K_I8                */
+    int32_t ternary;                          /* of both matrices                 */
+    bnn_expert_matrix main, up;               /* up.W NULL: none                  */
+    int32_t act;
+    const void* residual; int64_t ldr;        /* [positions, ldr >= N] in y_dtype, or NULL */
+    void* y; int64_t ldy; int32_t y_dtype;    /* [positions, ldy >= N]            */
+} bnn_expert_args;
+
+/* For every position p of expert e, with its INT8 row q and D = sum_k q[k] w[n,k]
+ * (exact int32):
+ *     z = fl32(fl32(alpha D) xscale) + bias          (of main; u likewise of up)
+ *     y[p,n] = act(z) (* u) (+ residual[p,n])
+ * in fp32, rounded once to y's type.  Positions from offsets[experts] on, and
+ * those whose order names no row, are left alone.  residual may be y.  Rows of
+ * residual and y need only the alignment of their type. */
+bnn_status bnn_expert_linear(const bnn_expert_args* args, bnn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,6 +30,7 @@ __all__ = [
     "W_TERNARY", "pack_weights_ternary", "EPI_SIGN_PACK", "pack_activations_rsign", "conv3x3_fused",
     "KVCache", "qk_norm_rope", "rope_turns", "tree_mask", "tree_attention", "tree_attention_workspace",
     "cache_score_add", "cache_evict", "cache_evict_workspace",
+    "block_norm", "expert_route", "expert_route_workspace", "ExpertWeights", "expert_linear",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbnn.so")
@@ -171,6 +172,54 @@ class _EvictArgs(ctypes.Structure):
     ]
 
 
+class _NormArgs(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("D", ctypes.c_int64), ("used", ctypes.c_void_p),
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_dtype", ctypes.c_int32),
+        ("branch", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("b_dtype", ctypes.c_int32), ("b_rows", ctypes.c_int64),
+        ("place", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("parts", ctypes.c_int64),
+        ("post", ctypes.c_int32), ("post_weight", ctypes.c_void_p), ("post_bias", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64),
+        ("x_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
+        ("pre", ctypes.c_int32), ("pre_weight", ctypes.c_void_p), ("pre_bias", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("x_out", ctypes.c_void_p), ("ldxo", ctypes.c_int64),
+        ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("y_dtype", ctypes.c_int32),
+        ("Xq", ctypes.c_void_p), ("ldXq", ctypes.c_int64), ("Xb", ctypes.c_void_p), ("ldXb", ctypes.c_int64),
+        ("xsum", ctypes.c_void_p), ("xscale", ctypes.c_void_p),
+    ]
+
+
+class _RouteArgs(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("rows", ctypes.c_int64), ("experts", ctypes.c_int64), ("top", ctypes.c_int64),
+        ("used", ctypes.c_void_p), ("score", ctypes.c_int32), ("bias", ctypes.c_void_p),
+        ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("expert", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+        ("order", ctypes.c_void_p), ("place", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
+class _ExpertMatrix(ctypes.Structure):
+    _fields_ = [
+        ("W", ctypes.c_void_p), ("alpha", ctypes.c_void_p), ("ld_alpha", ctypes.c_int64),
+        ("bias", ctypes.c_void_p), ("ld_bias", ctypes.c_int64),
+    ]
+
+
+class _ExpertArgs(ctypes.Structure):
+    _fields_ = [
+        ("Xq", ctypes.c_void_p), ("ldXq", ctypes.c_int64), ("xscale", ctypes.c_void_p), ("rows", ctypes.c_int64),
+        ("order", ctypes.c_void_p), ("per_row", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+        ("experts", ctypes.c_int64), ("positions", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("ternary", ctypes.c_int32), ("main", _ExpertMatrix), ("up", _ExpertMatrix), ("act", ctypes.c_int32),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+        ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("y_dtype", ctypes.c_int32),
+    ]
+
+
 _lib = None
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
@@ -214,6 +263,10 @@ def lib() -> ctypes.CDLL:
             "bnn_tree_attention": [_vp, _vp, _vp, _vp],
             "bnn_cache_score_add": [_vp, _vp, _vp, _vp],
             "bnn_cache_evict": [_vp, _vp, _vp, _vp],
+            "bnn_block_norm": [_vp, _vp],
+            "bnn_expert_route": [_vp, _vp],
+            "bnn_expert_pack": [_vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp],
+            "bnn_expert_linear": [_vp, _vp],
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -223,6 +276,10 @@ def lib() -> ctypes.CDLL:
         L.bnn_tree_attention_workspace.restype = _i64
         L.bnn_cache_evict_workspace.argtypes = [_vp, _i64]
         L.bnn_cache_evict_workspace.restype = _i64
+        L.bnn_expert_route_workspace.argtypes = [_i64, _i64, _i64]
+        L.bnn_expert_route_workspace.restype = _i64
+        L.bnn_expert_pack_bytes.argtypes = [_i64, _i64, _i64, ctypes.c_int32]
+        L.bnn_expert_pack_bytes.restype = _i64
         _lib = L
     return _lib
 
@@ -919,3 +976,269 @@ def cache_evict(cache: KVCache, indptr: torch.Tensor, ctx: torch.Tensor, *, budg
     _check((_lib or lib()).bnn_cache_evict(cache._ref, _batch(cache, indptr, ctx, 1 << 30, max_nodes, max_ctx), a, _raw_stream(cache._index)),
            "bnn_cache_evict")
     return ctx_out
+
+
+# ---- the decoder's feed-forward half
+#
+# Also calls of a few microseconds: packed argument structs, checks that test
+# what is right first.
+
+_pack_norm, _pack_route = (_layout(t).pack for t in (_NormArgs, _RouteArgs))
+# bnn_expert_args with its two matrices in line; each member of both is 8 bytes
+_pack_expert = struct.Struct("@PqPqPqPqqqqiPPqPqPPqPqiPqPqi").pack
+assert struct.calcsize("@PqPqPqPqqqqiPPqPqPPqPqiPqPqi") == _ExpertArgs.y_dtype.offset + 4
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
+_TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+MAX_NORM_D = 16384
+MAX_EXPERTS = 1024
+
+
+def _one_of(kinds: dict, value: str, name: str) -> int:
+    if value not in kinds:
+        raise ValueError(f"{name} must be one of {sorted(kinds)} (got {value!r})")
+    return kinds[value]
+
+
+def _float_type(t: torch.Tensor, name: str) -> int:
+    kind = _TYPES.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be torch.float32, torch.bfloat16 or torch.float16 (got {t.dtype})")
+    return kind
+
+
+def _matrix(t: torch.Tensor, dtype, name: str, rows: int, cols: int, index: int):
+    """Address and row stride of a [rows, cols] matrix on device `index`."""
+    if not (t.dtype is dtype and t.get_device() == index and t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols):
+        _dev(t, dtype, name)
+        raise ValueError(f"{name} must be [{rows}, {cols}] on cuda:{index} (got {tuple(t.shape)} on {t.device})")
+    row, col = t.stride()
+    if col != 1 and cols > 1 and rows > 0:
+        raise ValueError(f"{name} must have a unit column stride")
+    return t.data_ptr() or _EMPTY, row if rows > 1 else max(row, cols)
+
+
+def _vector(t: torch.Tensor | None, dtype, name: str, n: int, index: int) -> int:
+    """Address of a vector of n elements on device `index`; 0 for None."""
+    if t is None:
+        return 0
+    if t.get_device() != index:
+        _dev(t, dtype, name)
+        raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
+    return _flat(t, dtype, name, n)
+
+
+def _on(index: int, call, *args) -> int:
+    """The status of a call that launches on device `index`, on its current stream."""
+    if index == torch.cuda.current_device():
+        return call(*args, _raw_stream(index))
+    with torch.cuda.device(index):
+        return call(*args, _raw_stream(index))
+
+
+def block_norm(x: torch.Tensor | None = None, branch: torch.Tensor | None = None, *, place: torch.Tensor | None = None,
+               weight: torch.Tensor | None = None, post: str = "none", post_weight: torch.Tensor | None = None,
+               post_bias: torch.Tensor | None = None, gate: torch.Tensor | None = None, x_scale: float = 1.0,
+               branch_scale: float = 1.0, pre: str = "rms", pre_weight: torch.Tensor | None = None,
+               pre_bias: torch.Tensor | None = None, eps: float = 1e-6, used: torch.Tensor | None = None,
+               y_dtype: torch.dtype | None = None, int8: bool = True, planes: bool = False, out: dict | None = None) -> dict:
+    """What lies between two linear layers of a block, in one pass
+    (bnn_block_norm):
+
+        b = sum_j weight[:, j] * branch[place[:, j]]       (or branch)
+        x = x_scale * x + branch_scale * gate * post(b);   y = pre(x);   INT8 rows of y
+
+    ``x`` [M, D] (the residual stream) and ``branch`` [M, D], or [rows, D]
+    with ``place`` int32 and ``weight`` float32 [M, parts] (as expert_route
+    gives them): float32, bfloat16 or float16, either may be left out.
+    ``post``, ``pre``: "none", "rms" or "layer", with float32 [D] weights and
+    biases (None: 1 and 0).  ``gate``: float32 [D] or [M, D].  ``used``: int32
+    [1], the rows from there on are left alone.
+
+    Returns a dict: ``x`` (the new stream, where x and branch are given),
+    ``y`` in ``y_dtype`` (where given), with ``int8`` ``Xq``, with ``planes``
+    ``Xb`` and ``xsum``, with either ``xscale``, as quantize_act_i8 gives
+    them.  ``out``: such a dict of tensors to write instead; it then says by
+    itself which outputs there are (``out["x"]`` may be ``x``)."""
+    first = x if x is not None else branch
+    if first is None:
+        raise ValueError("x or branch must be given")
+    index = _dev(first, first.dtype, "x or branch").get_device()
+    D = first.shape[-1]
+    M = x.shape[0] if x is not None else place.shape[0] if place is not None else branch.shape[0]
+    if out is None:
+        dev = first.device
+        out = {}
+        if x is not None and branch is not None:
+            out["x"] = torch.empty((M, D), dtype=x.dtype, device=dev)
+        if y_dtype is not None:
+            out["y"] = torch.empty((M, D), dtype=y_dtype, device=dev)
+        if int8:
+            out["Xq"] = torch.empty((M, i8_ld(D)), dtype=torch.int8, device=dev)[:, :D]
+        if planes:
+            out["Xb"] = torch.empty((M, 8, padded_ld(D)), dtype=torch.int32, device=dev)
+            out["xsum"] = torch.empty(M, dtype=torch.int32, device=dev)
+        if int8 or planes:
+            out["xscale"] = torch.empty(M, dtype=torch.float32, device=dev)
+    get = out.get
+    xo, y, Xq, Xb, xsum, xscale = get("x"), get("y"), get("Xq"), get("Xb"), get("xsum"), get("xscale")
+    xp, bp, op, yp, qp, gp = (0, 0), (0, 0), (0, 0), (0, 0), (0, 0), (0, 0)
+    xt = bt = yt = b_rows = parts = 0
+    if x is not None:
+        xt = _float_type(x, "x")
+        xp = _matrix(x, x.dtype, "x", M, D, index)
+    if branch is not None:
+        bt = _float_type(branch, "branch")
+        b_rows = branch.shape[0] if place is not None else M
+        bp = _matrix(branch, branch.dtype, "branch", b_rows, D, index)
+    if xo is not None:
+        if x is not None and xo.dtype is not x.dtype:
+            raise TypeError(f"out['x'] must be {x.dtype} (got {xo.dtype})")
+        xt = _float_type(xo, "out['x']")
+        op = _matrix(xo, xo.dtype, "out['x']", M, D, index)
+    if y is not None:
+        yt = _float_type(y, "out['y']")
+        yp = _matrix(y, y.dtype, "out['y']", M, D, index)
+    if Xq is not None:
+        qp = _matrix(Xq, torch.int8, "out['Xq']", M, D, index)
+    bits = (0, 0)
+    if Xb is not None:
+        if _dev(Xb, torch.int32, "out['Xb']").dim() != 3 or Xb.shape[0] != M or Xb.get_device() != index:
+            raise ValueError(f"out['Xb'] must be [{M}, 8, ld] on cuda:{index}")
+        bits = Xb.data_ptr() or _EMPTY, _planes_ld(Xb)
+    if place is not None:
+        parts = place.shape[1]
+    elif weight is not None:
+        raise ValueError("weight goes with place")
+    if gate is not None:
+        gp = (_vector(gate, torch.float32, "gate", D, index), 0) if gate.dim() == 1 else _matrix(gate, torch.float32, "gate", M, D, index)
+    f32, i32 = torch.float32, torch.int32
+
+    a = _pack_norm(M, D, _vector(used, i32, "used", 1, index), *xp, xt, *bp, bt, b_rows, _vector(place, i32, "place", M * parts, index),
+                   _vector(weight, f32, "weight", M * parts, index), parts, _one_of(NORMS, post, "post"),
+                   _vector(post_weight, f32, "post_weight", D, index), _vector(post_bias, f32, "post_bias", D, index), *gp, x_scale, branch_scale,
+                   _one_of(NORMS, pre, "pre"), _vector(pre_weight, f32, "pre_weight", D, index), _vector(pre_bias, f32, "pre_bias", D, index), eps,
+                   *op, *yp, yt, *qp, *bits, _vector(xsum, i32, "out['xsum']", M, index), _vector(xscale, f32, "out['xscale']", M, index))
+    _check(_on(index, (_lib or lib()).bnn_block_norm, a), "bnn_block_norm")
+    return out
+
+
+def expert_route_workspace(rows: int, experts: int, top: int, *, device="cuda") -> torch.Tensor:
+    """A workspace for expert_route calls of up to these rows and experts."""
+    n = lib().bnn_expert_route_workspace(rows, experts, top)
+    if n < 0:
+        raise ValueError("expert_route_workspace: sizes out of range")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def expert_route(logits: torch.Tensor, top: int, *, score: str = "softmax", bias: torch.Tensor | None = None, renorm: bool = False,
+                 scale: float = 1.0, used: torch.Tensor | None = None, out: dict | None = None, workspace: torch.Tensor | None = None) -> dict:
+    """The experts of every token and the tokens sorted by expert
+    (bnn_expert_route).
+
+    ``logits`` [rows, experts] in float32, bfloat16 or float16.  ``score``:
+    "softmax" (over all experts) or "sigmoid".  ``bias`` float32 [experts] is
+    added to the scores for the choice only.  ``renorm``: weights divided by
+    their sum.  ``used``: int32 [1], rows from there on have no experts.
+
+    Returns a dict: ``expert`` int32 and ``weight`` float32 [rows, top],
+    ``offsets`` int32 [experts + 1] (expert e has the positions offsets[e] ..
+    offsets[e + 1] - 1), ``order`` int32 [rows * top] (row * top + choice of
+    each position), ``place`` int32 [rows, top] (its inverse; -1: none).
+    ``out``: such a dict of tensors to write instead.  ``workspace``:
+    expert_route_workspace, made here where it is None."""
+    rows, experts = logits.shape
+    L = _lib or lib()
+    if out is None:
+        pair = dict(dtype=torch.int32, device=logits.device)
+        out = {"expert": torch.empty((rows, top), **pair), "weight": torch.empty((rows, top), dtype=torch.float32, device=logits.device),
+               "offsets": torch.empty(experts + 1, **pair), "order": torch.empty(rows * top, **pair), "place": torch.empty((rows, top), **pair)}
+    if workspace is None:
+        workspace = torch.empty(max(0, L.bnn_expert_route_workspace(rows, experts, top)), dtype=torch.uint8, device=logits.device)
+    n, index, i32 = rows * top, _dev(logits, logits.dtype, "logits").get_device(), torch.int32
+    a = _pack_route(*_matrix(logits, logits.dtype, "logits", rows, experts, index), _float_type(logits, "logits"), rows, experts, top,
+                    _vector(used, i32, "used", 1, index), _one_of(SCORES, score, "score"), _vector(bias, torch.float32, "bias", experts, index),
+                    1 if renorm else 0, scale, _vector(out["expert"], i32, "out['expert']", n, index),
+                    _vector(out["weight"], torch.float32, "out['weight']", n, index), _vector(out["offsets"], i32, "out['offsets']", experts + 1, index),
+                    _vector(out["order"], i32, "out['order']", n, index), _vector(out["place"], i32, "out['place']", n, index),
+                    workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(_on(index, L.bnn_expert_route, a), "bnn_expert_route")
+    return out
+
+
+class ExpertWeights:
+    """One matrix for each expert as expert_linear reads it, laid out once
+    from packed planes (bnn_expert_pack).
+
+    ``Wp``, ``Zp``: the planes of pack_weights (``Zp`` None) or
+    pack_weights_ternary, [N, ld] of a single layer or [experts, N, ld]
+    stacked.  ``alpha`` float32 [experts, N] ([N] of a single layer), or
+    [experts] with one scale for a whole matrix; ``bias`` float32 like
+    [experts, N], or None.  The planes are not needed afterwards."""
+
+    def __init__(self, Wp: torch.Tensor, K: int, *, Zp: torch.Tensor | None = None, alpha: torch.Tensor, bias: torch.Tensor | None = None):
+        _dev(Wp, torch.int32, "Wp")
+        if Wp.dim() == 2:
+            Wp = Wp[None]
+            Zp = Zp[None] if Zp is not None and Zp.dim() == 2 else Zp
+        if Wp.dim() != 3 or Wp.stride(2) != 1:
+            raise ValueError("Wp must be [N, ld] or [experts, N, ld] with a unit last stride")
+        if Zp is not None and (_dev(Zp, torch.int32, "Zp").shape != Wp.shape or Zp.stride() != Wp.stride()):
+            raise ValueError("Zp must be laid out as Wp")
+        self.experts, self.N, self.K, self.ternary = Wp.shape[0], Wp.shape[1], int(K), Zp is not None
+        self.device = Wp.device
+        n = lib().bnn_expert_pack_bytes(self.experts, self.N, self.K, self.ternary)
+        if n < 0:
+            raise ValueError("ExpertWeights: sizes out of range")
+        self.W = torch.empty(n, dtype=torch.uint8, device=Wp.device)
+        index = self._index = Wp.get_device()
+        _check(_on(index, lib().bnn_expert_pack, Wp.data_ptr() or _EMPTY, 0 if Zp is None else Zp.data_ptr() or _EMPTY, Wp.stride(1), Wp.stride(0),
+                   self.experts, self.N, self.K, self.W.data_ptr() or _EMPTY, n), "bnn_expert_pack")
+        _dev(alpha, torch.float32, "alpha")
+        if alpha.shape == (self.N,) and self.experts == 1 and self.N != 1:
+            alpha = alpha[None]
+        if alpha.shape == (self.experts,):
+            scale = _vector(alpha, torch.float32, "alpha", self.experts, index), 0
+        else:
+            scale = _matrix(alpha, torch.float32, "alpha", self.experts, self.N, index)
+        shift = 0, 0
+        if bias is not None:
+            shift = _matrix(bias[None] if bias.dim() == 1 else bias, torch.float32, "bias", self.experts, self.N, index)
+        self.alpha, self.bias = alpha, bias
+        self._c = (self.W.data_ptr() or _EMPTY, *scale, *shift)
+
+
+def expert_linear(Xq: torch.Tensor, weights: ExpertWeights, *, xscale: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
+                  order: torch.Tensor | None = None, per_row: int = 1, up: ExpertWeights | None = None, act: str = "none",
+                  residual: torch.Tensor | None = None, out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """INT8 rows times the matrix of each row's expert (bnn_expert_linear):
+
+        y = act(alpha * D * xscale + bias) [* (the same of ``up``)] [+ residual],   D = Xq W^T
+
+    ``Xq`` int8 [rows, K] with a row stride of a multiple of 16 and ``xscale``
+    float32 [rows], as quantize_act_i8 and block_norm give them.
+    ``offsets``: int32 [experts + 1], the positions of each expert (None with a
+    single matrix: all).  ``order`` int32 [positions]: position p reads row
+    order[p] // per_row (expert_route's order and top); None: row p.  ``act``:
+    "none", "relu", "relu2", "silu", "gelu" or "gelu_tanh".  ``residual``:
+    [positions, N] in the output's type.  Returns ``out`` [positions, N] in
+    ``out_dtype`` (float32, bfloat16 or float16); positions past the last
+    expert's are left alone."""
+    rows = Xq.shape[0]
+    K, N, experts = weights.K, weights.N, weights.experts
+    positions = rows if order is None else order.numel()
+    if out is None:
+        out = Xq.new_empty((positions, N), dtype=out_dtype)
+    if up is not None and (up._index != weights._index or up.K != K or up.N != N or up.experts != experts or up.ternary != weights.ternary):
+        raise ValueError("up must have the sizes, the kind and the device of weights")
+    kind = out.dtype
+    index = weights._index
+    a = _pack_expert(*_matrix(Xq, torch.int8, "Xq", rows, K, index), _vector(xscale, torch.float32, "xscale", rows, index), rows,
+                     _vector(order, torch.int32, "order", positions, index), per_row, _vector(offsets, torch.int32, "offsets", experts + 1, index),
+                     experts, positions, N, K, 1 if weights.ternary else 0, *weights._c, *(up._c if up is not None else (0, 0, 0, 0, 0)),
+                     _one_of(ACTIVATIONS, act, "act"), *((0, 0) if residual is None else _matrix(residual, kind, "residual", positions, N, index)),
+                     *_matrix(out, kind, "out", positions, N, index), _float_type(out, "out"))
+    _check(_on(index, (_lib or lib()).bnn_expert_linear, a), "bnn_expert_linear")
+    return out

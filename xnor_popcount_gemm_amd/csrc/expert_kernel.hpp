@@ -1,0 +1,186 @@
+// What the kernels of the grouped products share: which expert and positions a
+// tile has, the expansion of packed weights, the epilogue.
+#pragma once
+
+#include "ffn.hpp"
+
+namespace bnn {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+// 4 weights as bytes -1, 0, +1: codes at bits 2 d + {0, 8, 16, 24} of a
+// ternary word, d < 4, or at bits d + {0, 8, 16, 24} of a binary one, d < 8.
+template <bool TERN>
+__device__ __forceinline__ int expand4(uint32_t w, int d) {
+    return TERN ? (int)__builtin_amdgcn_perm(0u, 0xFF000100u, (w >> (2 * d)) & 0x03030303u)
+                : (int)__builtin_amdgcn_perm(0u, 0x0000FF01u, (w >> d) & 0x01010101u);
+}
+
+// The 16 bytes of a lane's fragment of 64-k step s of its chunk.
+template <bool TERN>
+__device__ __forceinline__ v4i expand16(const uint32_t (&w)[4], int s) {
+    v4i r;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) r[d] = TERN ? expand4<true>(w[s], d) : expand4<false>(w[s >> 1], 4 * (s & 1) + d);
+    return r;
+}
+
+// 16 bytes of an INT8 row from k on (a multiple of 16), 0 from K on.  A piece
+// that begins below K ends within the row's stride, a multiple of 16.
+__device__ __forceinline__ v4i masked16(const int8_t* row, int k, int K) {
+    v4i v = {0, 0, 0, 0};
+    if (k >= K) return v;
+    v = *(const v4i*)(row + k);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const int left = K - k - 4 * d;
+        v[d] &= left >= 4 ? ~0 : left <= 0 ? 0 : (int)((1u << (8 * left)) - 1u);
+    }
+    return v;
+}
+
+// Tile `slot` of the positions cut into tiles of `size` within each expert:
+// expert (-1: there are no so many tiles), first position, positions.  Every lane of the
+// wave calls it.
+struct Tile {
+    int e, p0, n;
+};
+
+__device__ __forceinline__ Tile find_tile(const ExpertArgs& a, int slot, int size) {
+    if (!a.offsets) {
+        const int p0 = slot * size;
+        return p0 < a.positions ? Tile{0, p0, min(size, a.positions - p0)} : Tile{-1, 0, 0};
+    }
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 64) {
+        const int e = e0 + lane;
+        int lo = 0, hi = 0;
+        if (e < a.experts) {   // offsets out of order or range give no positions
+            lo = max(a.offsets[e], 0);
+            hi = min(a.offsets[e + 1], a.positions);
+        }
+        const int n = hi > lo ? (hi - lo + size - 1) / size : 0;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(sum, d, 64);
+            if (lane >= d) sum += o;
+        }
+        const uint64_t past = __ballot(before + sum > slot);
+        if (past) {
+            const int at = __ffsll((unsigned long long)past) - 1;
+            const int i = slot - before - __shfl(sum - n, at, 64), end = __shfl(hi, at, 64);
+            const int64_t p0 = __shfl(lo, at, 64) + (int64_t)i * size;
+            if (i < 0 || p0 >= end) return {-1, 0, 0};   // offsets that decrease
+            return {__builtin_amdgcn_readfirstlane(e0 + at), __builtin_amdgcn_readfirstlane((int)p0),
+                    __builtin_amdgcn_readfirstlane(min(size, end - (int)p0))};
+        }
+        before += __shfl(sum, 63, 64);
+    }
+    return {-1, 0, 0};
+}
+
+// Tiles that cover any offsets.
+inline int64_t tile_slots(const ExpertArgs& a, int64_t size) {
+    const int64_t p = a.positions, e = a.experts < p ? a.experts : p;
+    if (!a.offsets) return (p + size - 1) / size;
+    const int64_t n = (p + e * (size - 1)) / size;
+    return n < p ? n : p;
+}
+
+// Row of Xq of a position; -1: none.
+__device__ __forceinline__ int source_row(const ExpertArgs& a, int p) {
+    if (!a.order) return p;
+    const int o = a.order[p];
+    const uint32_t r = o < 0 ? 0xFFFFFFFFu : fastdiv((uint32_t)o, a.per_row);
+    return r < (uint32_t)a.rows ? (int)r : -1;
+}
+
+enum : int32_t { ACT_NONE = 0, ACT_RELU = 1, ACT_RELU2 = 2, ACT_SILU = 3, ACT_GELU = 4, ACT_GELU_TANH = 5 };
+
+__device__ __forceinline__ float activate(float z, int act) {
+    switch (act) {
+    case ACT_RELU: return z < 0.f ? 0.f : z;   // NaN stays
+    case ACT_RELU2: return z < 0.f ? 0.f : z * z;
+    case ACT_SILU: return z / (1.f + expf(-z));
+    case ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case ACT_GELU_TANH: {
+        const float t = 1.5957691216057308f * (z + 0.044715f * z * z * z);   // 1 + tanh(t / 2) = 2 / (1 + exp(-t))
+        return z / (1.f + expf(-t));
+    }
+    default: return z;
+    }
+}
+
+// alpha[n .. n+3] and the like of expert e; entries past N are not read.
+__device__ __forceinline__ f32x4 row4(const float* p, int64_t ld, int e, int n, int N) {
+    const float* q = p + (int64_t)e * ld + n;
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < N) v[i] = q[i];
+    return v;
+}
+
+// alpha and bias of 4 columns of a matrix.
+struct Scale4 {
+    f32x4 alpha, bias;
+    bool has_bias;
+};
+
+__device__ __forceinline__ Scale4 scale4(const ExpertMatrix& m, int e, int n, int N) {
+    Scale4 s;
+    if (m.ld_alpha == 0) s.alpha = f32x4{} + m.alpha[e];
+    else s.alpha = row4(m.alpha, m.ld_alpha, e, n, N);
+    s.has_bias = m.bias != nullptr;
+    s.bias = s.has_bias ? row4(m.bias, m.ld_bias, e, n, N) : f32x4{0, 0, 0, 0};
+    return s;
+}
+
+__device__ __forceinline__ f32x4 scaled4(v4i d, const Scale4& s, float xs, bool has_xs) {
+    f32x4 z = s.alpha * __builtin_convertvector(d, f32x4);
+    if (has_xs) z = z * xs;
+    if (s.has_bias) z = z + s.bias;
+    return z;
+}
+
+template <typename E>
+__device__ __forceinline__ void finish4(const ExpertArgs& a, int p, int n, f32x4 v) {
+    typedef E e4 __attribute__((ext_vector_type(4)));
+    if (a.r) {
+        const E* r = (const E*)a.r + (int64_t)p * a.ldr + n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < a.N) v[i] += (float)r[i];
+    }
+    E* y = (E*)a.y + (int64_t)p * a.ldy + n;
+    if (n + 4 <= a.N && (reinterpret_cast<uintptr_t>(y) & (4 * sizeof(E) - 1)) == 0) {
+        *(e4*)y = __builtin_convertvector(v, e4);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < a.N) y[i] = (E)v[i];
+    }
+}
+
+// Columns n .. n+3 of position p from the sums.
+template <bool GATED>
+__device__ __forceinline__ void finish(const ExpertArgs& a, int p, int src, int n, v4i d, v4i du, const Scale4& s, const Scale4& su) {
+    const bool has_xs = a.xscale != nullptr;
+    const float xs = has_xs ? a.xscale[src] : 1.f;
+    f32x4 z = scaled4(d, s, xs, has_xs);
+    if (a.act != ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = activate(z[i], a.act);
+    }
+    if (GATED) z = z * scaled4(du, su, xs, has_xs);
+    if (a.y_type == T_F32) finish4<float>(a, p, n, z);
+    else if (a.y_type == T_BF16) finish4<__bf16>(a, p, n, z);
+    else finish4<_Float16>(a, p, n, z);
+}
+
+bool expert_rows_fits(const ExpertArgs& a, bool ternary);
+hipError_t launch_expert_rows(const ExpertArgs& a, bool ternary, hipStream_t s);
+
+}  // namespace bnn
