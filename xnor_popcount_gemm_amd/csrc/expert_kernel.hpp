@@ -81,6 +81,19 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& a, int slot, int siz
     return {-1, 0, 0};
 }
 
+// How many tiles of `size` the offsets make.  Every lane of the wave calls it.
+__device__ __forceinline__ int tile_count(const ExpertArgs& a, int size) {
+    if (!a.offsets) return (a.positions + size - 1) / size;
+    int sum = 0;
+    for (int e = threadIdx.x & 63; e < a.experts; e += 64) {
+        const int lo = max(a.offsets[e], 0), hi = min(a.offsets[e + 1], a.positions);
+        sum += hi > lo ? (hi - lo + size - 1) / size : 0;
+    }
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s, 64);
+    return __builtin_amdgcn_readfirstlane(sum);
+}
+
 // Tiles that cover any offsets.
 inline int64_t tile_slots(const ExpertArgs& a, int64_t size) {
     const int64_t p = a.positions, e = a.experts < p ? a.experts : p;
@@ -164,11 +177,10 @@ __device__ __forceinline__ void finish4(const ExpertArgs& a, int p, int n, f32x4
     }
 }
 
-// Columns n .. n+3 of position p from the sums.
+// Columns n .. n+3 of position p, whose row has the scale xs, from the sums.
 template <bool GATED>
-__device__ __forceinline__ void finish(const ExpertArgs& a, int p, int src, int n, v4i d, v4i du, const Scale4& s, const Scale4& su) {
+__device__ __forceinline__ void finish(const ExpertArgs& a, int p, float xs, int n, v4i d, v4i du, const Scale4& s, const Scale4& su) {
     const bool has_xs = a.xscale != nullptr;
-    const float xs = has_xs ? a.xscale[src] : 1.f;
     f32x4 z = scaled4(d, s, xs, has_xs);
     if (a.act != ACT_NONE) {
 #pragma unroll
@@ -182,5 +194,7 @@ __device__ __forceinline__ void finish(const ExpertArgs& a, int p, int src, int 
 
 bool expert_rows_fits(const ExpertArgs& a, bool ternary);
 hipError_t launch_expert_rows(const ExpertArgs& a, bool ternary, hipStream_t s);
+bool expert_tile_takes(const ExpertArgs& a);
+hipError_t launch_expert_tile(const ExpertArgs& a, bool ternary, hipStream_t s);
 
 }  // namespace bnn

@@ -86,7 +86,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_expert_rows(ExpertArgs a, int fr
         if (GATED)
 #pragma unroll
             for (int v = 0; v < WAVES; ++v) du += part[v][(H - 1) * MT + i][lane];
-        finish<GATED>(a, p, src, n, d, du, scale4(a.m, t.e, n, a.N), GATED ? scale4(a.u, t.e, n, a.N) : Scale4{});
+        finish<GATED>(a, p, a.xscale ? a.xscale[src] : 1.f, n, d, du, scale4(a.m, t.e, n, a.N), GATED ? scale4(a.u, t.e, n, a.N) : Scale4{});
     }
 }
 

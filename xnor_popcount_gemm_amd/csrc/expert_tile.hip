@@ -1,0 +1,267 @@
+// Grouped products with many rows to an expert: tiles of 64 to 256 positions x
+// 256 weight rows (128 of each matrix with a gate) on the int8 matrix cores.
+//
+//     D[p, n] = sum_k q[row(p), k] w_e[n, k]    (exact int32), then the epilogue
+//
+// Bound by the matrix cores and what feeds them.  Four waves share the tile by
+// weight rows: each has all its positions and 64 weight rows, so that every
+// weight is expanded by one wave only, in registers, straight from global
+// memory (a chunk of 256 or 512 k ahead), and serves 4 to 16 matrix
+// instructions.  Only the INT8 rows go through LDS: stages of 128 k, brought
+// by loads to LDS three stages ahead of their use (a ring of four), the
+// 16-byte pieces of a row permuted by the row so that the 8 lanes that are
+// served together fall on distinct banks.  LDS reads are 64 KiB a 64-k step
+// for 256 positions, half of what the matrix cores' time allows.  Weights are
+// the rows of an instruction and positions its columns: a lane ends with 4
+// neighbouring outputs of a position.
+//
+// Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous run of the
+// tiles, in groups of 8 position tiles by weight tile, so that what is in its
+// L2 is used again.
+#include <type_traits>
+
+#include "expert_kernel.hpp"
+
+namespace bnn {
+namespace {
+
+constexpr int FN = 4;                       // weight fragments of a wave
+constexpr int ST = 128, RING = 4;           // k of a stage; stages in LDS
+
+typedef __attribute__((address_space(3))) void* lptr_t;
+#define INLINE __attribute__((always_inline))   // lambdas that are called from many places and hold references to the sums
+
+template <int I> using Ic = std::integral_constant<int, I>;
+
+// s_waitcnt that leaves at most n vector-memory operations outstanding (vmcnt
+// in bits 3:0 and 15:14) and does not wait for the other counters.
+constexpr unsigned vmcnt(int n) { return (unsigned)(n & 0xF) | ((unsigned)((n >> 4) & 3) << 14) | (0x7u << 4) | (0xFu << 8); }
+
+// A barrier without the fence of __syncthreads(), which would wait for every
+// load to LDS in flight.  The caller has waited for its loads that the others
+// read next, and what it read from LDS has gone into matrix instructions.
+__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+
+// RW waves share the positions, each with MF fragments of 16, and four the weight rows.
+template <bool TERN, bool GATED, int RW, int MF>
+__global__ __launch_bounds__(256 * RW, 2) void k_expert_tile(ExpertArgs a, int frags, int chunks, int tiles_n, uint32_t x_bytes) {
+    constexpr int THREADS = 256 * RW, BM = 16 * MF * RW, CK = chunk_k(TERN), CS = CK / ST;   // stages of a weight chunk
+    constexpr int PIECES = BM * ST / 16 / THREADS;                  // 16-byte loads of a lane for a stage
+    __shared__ __attribute__((aligned(16))) int8_t lds0[BM * ST], lds1[BM * ST], lds2[BM * ST], lds3[BM * ST];
+    auto buf = [&](auto I) -> int8_t* {
+        constexpr int i = decltype(I)::value % RING;
+        if constexpr (i == 0) return lds0;
+        else if constexpr (i == 1) return lds1;
+        else if constexpr (i == 2) return lds2;
+        else return lds3;
+    };
+    __shared__ int source[BM];
+    __shared__ float factor[BM];
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 3, wr = wave >> 2;
+
+    // which tile
+    const int slots = tile_count(a, BM);
+    const int total = slots * tiles_n, run = (total + 7) / 8;
+    const int place = (int)(blockIdx.x >> 3), tile = (int)(blockIdx.x & 7) * run + place;
+    if (place >= run || tile >= total) return;
+    constexpr int GROUP = 8;
+    const int grp = tile / (GROUP * tiles_n), first = grp * GROUP, size = min(slots - first, GROUP), in = tile - first * tiles_n;
+    const Tile t = find_tile(a, first + in % size, BM);
+    if (t.e < 0) return;
+    const int tn = in / size;
+
+    if (tid < t.n) {
+        const int src = source_row(a, t.p0 + tid);
+        source[tid] = src;
+        factor[tid] = a.xscale && src >= 0 ? a.xscale[src] : 1.f;
+    }
+
+    // INT8 rows: load i of the wave brings tile rows 8 (PIECES wave + i) .. + 7, lane l the piece of row l / 8
+    // that belongs at place l % 8
+    const __amdgpu_buffer_rsrc_t xr = rsrc_of(a.Xq, x_bytes);
+    uint32_t off[PIECES];
+    const uint32_t piece = (uint32_t)(((lane & 7) ^ (lane >> 3)) << 4);
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int row = 8 * (PIECES * wave + i) + (lane >> 3);
+        const int src = source_row(a, t.p0 + min(row, t.n - 1));
+        off[i] = (uint32_t)max(src, 0) * (uint32_t)a.ldXq + piece;
+    }
+    auto issue = [&](auto I, int s) INLINE {
+        int8_t* to = buf(I) + PIECES * wave * 1024;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lptr_t)(to + i * 1024), 16, (int)off[i], s * ST, 0, 0);
+    };
+    auto issue_last = [&](auto I, int s) INLINE {     // the stage that holds the rows' end, through registers
+        int8_t* to = buf(I) + PIECES * wave * 1024;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) *(v4i*)(to + i * 1024 + 16 * lane) = masked16(a.Xq + (off[i] - piece), s * ST + (int)piece, a.K);
+    };
+
+    // weights: fragment q of the wave, a chunk at a time
+    const uint4* w[FN];
+#pragma unroll
+    for (int q = 0; q < FN; ++q) {
+        const int f = GATED ? 8 * tn + 2 * wn + (q >> 1) : 16 * tn + 4 * wn + q;
+        w[q] = (GATED && (q & 1) ? a.u.W : a.m.W) + ((int64_t)t.e * frags + min(f, frags - 1)) * chunks * 64;
+    }
+    uint32_t now[FN][4], next[FN][4];
+    auto fetch = [&](int c) INLINE {
+        const int64_t to = (int64_t)min(c, chunks - 1) * 64;
+#pragma unroll
+        for (int q = 0; q < FN; ++q) {
+            const uint4 b = (w[q] + to)[lane];
+            next[q][0] = b.x; next[q][1] = b.y; next[q][2] = b.z; next[q][3] = b.w;
+        }
+    };
+
+    v4i acc[MF][FN];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int q = 0; q < FN; ++q) acc[i][q] = v4i{0, 0, 0, 0};
+    int at[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) at[u] = (16 * MF * wr + r16) * ST + (((4 * u + g) ^ (r16 & 7)) << 4);
+
+    // The two 64-k steps of stage P of a chunk group.
+    constexpr int AHEAD = 4;                   // row fragments that are read before their use
+    auto compute = [&](auto P) INLINE {
+        const int8_t* x = buf(P);
+        constexpr int step = 2 * (decltype(P)::value % CS);
+        v4i xv[AHEAD], b[FN];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) xv[i] = *(const v4i*)(x + at[0] + i * 16 * ST);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int q = 0; q < FN; ++q) b[q] = expand16<TERN>(now[q], step + u);
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                const int y = u * MF + i, z = y + AHEAD;
+#pragma unroll
+                for (int q = 0; q < FN; ++q) acc[i][q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[q], xv[y % AHEAD], acc[i][q], 0, 0, 0);
+                if (z < 2 * MF) xv[y % AHEAD] = *(const v4i*)(x + at[z / MF] + (z % MF) * 16 * ST);
+            }
+        }
+    };
+
+    const int stages = (a.K + ST - 1) / ST, full = a.K / ST;
+    auto issue_any = [&](auto I, int s) INLINE {
+        if (s < full) issue(I, s);
+        else if (s < stages) issue_last(I, s);
+    };
+    fetch(0);
+    issue_any(Ic<0>{}, 0);
+    issue_any(Ic<1>{}, 1);
+    issue_any(Ic<2>{}, 2);
+    auto turn_chunk = [&](int s) INLINE {
+#pragma unroll
+        for (int q = 0; q < FN; ++q)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) now[q][d] = next[q][d];
+        fetch(s / CS + 1);
+    };
+    // A stage whose loads, and those that it starts, lie within the rows: its
+    // own are there when those of the two stages after it, and of the weights
+    // that were asked for since, are outstanding.
+    auto fast_stage = [&](int s, auto P) INLINE {
+        constexpr int p = decltype(P)::value;
+        constexpr int asked = (p + 3) % CS == 0 || (CS == 4 && (p + 2) % CS == 0) || CS == 2 ? FN : 0;
+        __builtin_amdgcn_s_waitcnt(vmcnt(2 * PIECES + asked));
+        barrier();
+        if constexpr (p % CS == 0) turn_chunk(s);
+        issue(Ic<p + 3>{}, s + 3);
+        compute(P);
+    };
+    auto stage = [&](int s, auto P) INLINE {
+        constexpr int p = decltype(P)::value;
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if constexpr (p % CS == 0) turn_chunk(s);
+        issue_any(Ic<p + 3>{}, s + 3);
+        compute(P);
+    };
+    int s = 0;
+    for (; s + 6 < full; s += 4) {
+        fast_stage(s, Ic<0>{});
+        fast_stage(s + 1, Ic<1>{});
+        fast_stage(s + 2, Ic<2>{});
+        fast_stage(s + 3, Ic<3>{});
+    }
+    for (; s < stages; s += 4) {
+        stage(s, Ic<0>{});
+        if (s + 1 < stages) stage(s + 1, Ic<1>{});
+        if (s + 2 < stages) stage(s + 2, Ic<2>{});
+        if (s + 3 < stages) stage(s + 3, Ic<3>{});
+    }
+
+    // Epilogue.  The ring is free: each wave parks 32 columns of its sums at a time in a part of its own (16-byte
+    // pieces permuted by the row, as above) and reads them back row by row, so that neighbouring lanes store
+    // neighbouring columns and the code for an output stands here once.
+    int8_t* mine = (wn == 0 ? lds0 : wn == 1 ? lds1 : wn == 2 ? lds2 : lds3) + 16 * MF * wr * 128;
+#pragma unroll
+    for (int c = 0; c < FN / 2; ++c) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) *(v4i*)(mine + (16 * i + r16) * 128 + (((4 * h + g) ^ (r16 & 7)) << 4)) = acc[i][2 * c + h];
+        __syncthreads();
+        constexpr int LANES = GATED ? 4 : 8;          // of a row
+        const int f = GATED ? 8 * tn + 2 * wn + c : 16 * tn + 4 * wn + 2 * c;
+        const int j = lane % LANES, n = 16 * f + 4 * j;
+        if (n < a.N) {
+            const Scale4 sm = scale4(a.m, t.e, n, a.N), su = GATED ? scale4(a.u, t.e, n, a.N) : Scale4{};
+            const int first_row = 16 * MF * wr, rows = min(16 * MF, t.n - first_row);
+#pragma unroll 1
+            for (int row = lane / LANES; row < rows; row += 64 / LANES) {
+                if (source[first_row + row] < 0) continue;
+                const int8_t* at_row = mine + row * 128;
+                const v4i d = *(const v4i*)(at_row + ((j ^ (row & 7)) << 4));
+                const v4i du = GATED ? *(const v4i*)(at_row + (((4 + j) ^ (row & 7)) << 4)) : v4i{0, 0, 0, 0};
+                finish<GATED>(a, t.p0 + first_row + row, factor[first_row + row], n, d, du, sm, su);
+            }
+        }
+    }
+}
+
+int tile_rows(const ExpertArgs& a) {
+    const int64_t mean = a.positions / a.experts;
+    return mean >= 192 ? 256 : mean >= 96 ? 128 : 64;
+}
+
+int64_t tiles_of(const ExpertArgs& a) {
+    const int64_t cols = a.u.W ? 128 : 256;
+    return (tile_slots(a, tile_rows(a)) * ((a.N + cols - 1) / cols) + 7) / 8 * 8;
+}
+
+}  // namespace
+
+bool expert_tile_takes(const ExpertArgs& a) {
+    return (int64_t)a.rows * a.ldXq < ((int64_t)1 << 31) && tiles_of(a) < ((int64_t)1 << 24) && a.positions / a.experts > 48;
+}
+
+hipError_t launch_expert_tile(const ExpertArgs& a, bool ternary, hipStream_t s) {
+    const int cols = a.u.W ? 128 : 256, frags = (a.N + 15) / 16, chunks = (a.K + chunk_k(ternary) - 1) / chunk_k(ternary);
+    const int tiles_n = (a.N + cols - 1) / cols, rows = tile_rows(a);
+    const uint32_t x_bytes = (uint32_t)(a.rows * a.ldXq);
+    const dim3 grid((unsigned)tiles_of(a));
+    const bool gated = a.u.W != nullptr;
+#define BNN_TILE(T, G, RW, MF) hipLaunchKernelGGL((k_expert_tile<T, G, RW, MF>), grid, dim3(256 * RW), 0, s, a, frags, chunks, tiles_n, x_bytes)
+#define BNN_TILE_MF(T, G) \
+    do { if (rows == 256) BNN_TILE(T, G, 2, 8); else if (rows == 128) BNN_TILE(T, G, 1, 8); else BNN_TILE(T, G, 1, 4); } while (0)
+    if (ternary) { if (gated) BNN_TILE_MF(true, true); else BNN_TILE_MF(true, false); }
+    else         { if (gated) BNN_TILE_MF(false, true); else BNN_TILE_MF(false, false); }
+#undef BNN_TILE_MF
+#undef BNN_TILE
+    return hipGetLastError();
+}
+
+}  // namespace bnn

@@ -206,8 +206,10 @@ bnn_status bnn_expert_linear(const bnn_expert_args* a, bnn_stream_t stream) {
 
 namespace bnn {
 
-bool expert_linear_fits(const ExpertArgs& a, bool ternary) { return expert_rows_fits(a, ternary); }
+bool expert_linear_fits(const ExpertArgs& a, bool ternary) { return expert_tile_takes(a) || expert_rows_fits(a, ternary); }
 
-hipError_t launch_expert_linear(const ExpertArgs& a, bool ternary, hipStream_t s) { return launch_expert_rows(a, ternary, s); }
+hipError_t launch_expert_linear(const ExpertArgs& a, bool ternary, hipStream_t s) {
+    return expert_tile_takes(a) ? launch_expert_tile(a, ternary, s) : launch_expert_rows(a, ternary, s);
+}
 
 }  // namespace bnn
