@@ -7,12 +7,16 @@
 //
 // Bound by memory traffic: each value is read once, held in registers through
 // its three or four row sums, and written once.  All arithmetic up to fl32(y)
-// is in 64 bits (a 64-bit operation takes a lane as long as a 32-bit one
-// here, and there are about 20 a value against 5-17 bytes moved), so codes
-// and scales do not depend on the order of a sum.
+// is in 64 bits, so codes and scales do not depend on the order of a sum; that
+// costs about 10 of the 25 operations of a value.  8192 rows of 4096, fp32 stream + two
+// experts' rows -> stream, codes: 111 us, 5.1 TB/s, what a plain copy reaches;
+// one branch 79 us, 5.5 TB/s; 16384 rows of 11008 bfloat16 -> codes, 3 bytes
+// a value: 183 us, 3.0 TB/s, where the operations bound it.
 //
 // A row belongs to T threads (a wave, or up to 16 waves of a workgroup),
-// thread t holds the 4-value groups t, t + T, ... of it.
+// thread t holds the 4-value groups t, t + T, ... of it.  Rows are read and
+// written through buffer descriptors of their own length, which stand in for
+// the tests of the row's end: with those, every load had a branch, and waited.
 #include "bnn_device.hpp"
 #include "ffn.hpp"
 
@@ -21,59 +25,106 @@ namespace {
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
-// 4 values from element e0 on of a row of D, zeros past its end.
-template <typename E, typename V4>
-__device__ __forceinline__ f32x4 load4(const char* row, int e0, int D, bool vec) {
-    const E* p = (const E*)row + e0;
-    if (vec && e0 + 4 <= D) return __builtin_convertvector(*(const V4*)p, f32x4);
-    f32x4 v = {0, 0, 0, 0};
+// A row of `count` values of a type: loads past its end give zeros and stores
+// there are dropped, without a branch (VEC: 4 values at a time, count a
+// multiple of 4; otherwise one by one).
+template <bool VEC>
+struct Row {
+    __amdgpu_buffer_rsrc_t r;
+
+    __device__ __forceinline__ Row(const void* base, int64_t first, int count, int bytes) {   // the same in all lanes of a wave
+        const char* p = (const char*)base + first * bytes;
+        const uint64_t u = (uint64_t)__builtin_amdgcn_readfirstlane((int)((uint64_t)p >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint64_t)p);
+        r = __builtin_amdgcn_make_buffer_rsrc((void*)u, (short)0, base ? count * bytes : 0, 0x00020000);
+    }
+
+    // 4 values from e0 on as they are stored: 16 or 8 bytes.
+    __device__ __forceinline__ u32x4 load(int e0, int type) const {
+        u32x4 v = {0, 0, 0, 0};
+        if (type == T_F32) {
+            if (VEC) return __builtin_amdgcn_raw_buffer_load_b128(r, 4 * e0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (e0 + i < D) v[i] = (float)p[i];
-    return v;
+            for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b32(r, 4 * (e0 + i), 0, 0);
+        } else if (VEC) {
+            const u32x2 h = __builtin_amdgcn_raw_buffer_load_b64(r, 2 * e0, 0, 0);
+            v[0] = h[0]; v[1] = h[1];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i >> 1] |= (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, 2 * (e0 + i), 0, 0) << (16 * (i & 1));
+        }
+        return v;
+    }
+
+    __device__ __forceinline__ void store(int e0, int type, f32x4 v) const {
+        if (type == T_F32) {
+            if (VEC) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, 4 * e0, 0, 0);
+            else
+#pragma unroll
+                for (int i = 0; i < 4; ++i) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r, 4 * (e0 + i), 0, 0);
+        } else {
+            const u32x2 h = type == T_BF16 ? __builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4))
+                                           : __builtin_bit_cast(u32x2, __builtin_convertvector(v, f16x4));
+            if (VEC) __builtin_amdgcn_raw_buffer_store_b64(h, r, 2 * e0, 0, 0);
+            else
+#pragma unroll
+                for (int i = 0; i < 4; ++i) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(h[i >> 1] >> (16 * (i & 1))), r, 2 * (e0 + i), 0, 0);
+        }
+    }
+
+    __device__ __forceinline__ void store_bytes(int e0, uint32_t v) const {
+        if (VEC) __builtin_amdgcn_raw_buffer_store_b32(v, r, e0, 0, 0);
+        else
+#pragma unroll
+            for (int i = 0; i < 4; ++i) __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(v >> (8 * i)), r, e0 + i, 0, 0);
+    }
+
+    __device__ __forceinline__ f32x4 floats(int e0) const { return __builtin_bit_cast(f32x4, load(e0, T_F32)); }
+};
+
+__device__ __forceinline__ f32x4 values(u32x4 v, int type) {
+    if (type == T_F32) return __builtin_bit_cast(f32x4, v);
+    const u32x2 h = {v[0], v[1]};
+    return type == T_BF16 ? __builtin_convertvector(__builtin_bit_cast(bf16x4, h), f32x4) : __builtin_convertvector(__builtin_bit_cast(f16x4, h), f32x4);
 }
 
-template <typename E, typename V4>
-__device__ __forceinline__ void store4(char* row, int e0, int D, bool vec, f32x4 v) {
-    E* p = (E*)row + e0;
-    if (vec && e0 + 4 <= D) *(V4*)p = __builtin_convertvector(v, V4);
-    else
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (e0 + i < D) p[i] = (E)v[i];
-}
-
-// The same for a whole row share, the type chosen outside of the loop.
-template <int NI, int T>
-__device__ __forceinline__ void load_row(f32x4 (&v)[NI], const char* row, int t, int D, int type, bool vec) {
+// A thread's share of a row, the type chosen once.
+template <int NI, int T, bool VEC>
+__device__ __forceinline__ void load_row(u32x4 (&v)[NI], const Row<VEC>& row, int t, int type) {
     if (type == T_F32) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) v[i] = load4<float, f32x4>(row, 4 * (t + i * T), D, vec);
-    } else if (type == T_BF16) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) v[i] = load4<__bf16, bf16x4>(row, 4 * (t + i * T), D, vec);
+        for (int i = 0; i < NI; ++i) v[i] = row.load(4 * (t + i * T), T_F32);
     } else {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) v[i] = load4<_Float16, f16x4>(row, 4 * (t + i * T), D, vec);
+        for (int i = 0; i < NI; ++i) v[i] = row.load(4 * (t + i * T), T_BF16);
     }
 }
 
-template <int NI, int T>
-__device__ __forceinline__ void store_row(const f32x4 (&v)[NI], char* row, int t, int D, int type, bool vec) {
+template <int NI>
+__device__ __forceinline__ void to_values(f32x4 (&x)[NI], const u32x4 (&v)[NI], int type) {
     if (type == T_F32) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) store4<float, f32x4>(row, 4 * (t + i * T), D, vec, v[i]);
+        for (int i = 0; i < NI; ++i) x[i] = values(v[i], T_F32);
     } else if (type == T_BF16) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) store4<__bf16, bf16x4>(row, 4 * (t + i * T), D, vec, v[i]);
+        for (int i = 0; i < NI; ++i) x[i] = values(v[i], T_BF16);
     } else {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) store4<_Float16, f16x4>(row, 4 * (t + i * T), D, vec, v[i]);
+        for (int i = 0; i < NI; ++i) x[i] = values(v[i], T_F16);
     }
 }
 
-__device__ __forceinline__ float rounded(float v, int type) {
-    return type == T_F32 ? v : type == T_BF16 ? (float)(__bf16)v : (float)(_Float16)v;
+template <int NI, int T, bool VEC>
+__device__ __forceinline__ void store_row(const f32x4 (&v)[NI], const Row<VEC>& row, int t, int type) {
+    if (type == T_F32) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) row.store(4 * (t + i * T), T_F32, v[i]);
+    } else if (type == T_BF16) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) row.store(4 * (t + i * T), T_BF16, v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) row.store(4 * (t + i * T), T_F16, v[i]);
+    }
 }
 
 // Sum of a value over the T threads of a row.  Every thread of the workgroup
@@ -93,173 +144,257 @@ __device__ __forceinline__ double row_sum(double v, double (*red)[T / 64], int& 
     return s;
 }
 
-template <int NI, int T>
-__device__ __forceinline__ void norm_row(double (&v)[NI][4], int kind, const float* w, const float* b, bool vw, bool vb, float eps, int t, int D,
-                                         double (*red)[T / 64], int& turn) {
-    if (kind == NORM_NONE) return;
-    if (kind == NORM_LAYER) {
-        double s = 0;
+// Values are widened to 64 bits again where they are used again: held wide over
+// a row sum they would take twice the registers, and registers are what limits
+// the rows in flight.
+template <int NI, typename H>
+__device__ __forceinline__ void afresh(H (&v)[NI][4]) {
+    if (sizeof(H) == 4)
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s += v[i][c];
-        const double mean = row_sum<T>(s, red, turn) / D;
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[i][c] = 4 * (t + i * T) + c < D ? v[i][c] - mean : 0.0;
-    }
+            for (int c = 0; c < 4; ++c) asm volatile("" : "+v"(v[i][c]));
+}
+
+// What a norm takes off and multiplies with.
+struct Norm {
+    double mean, inv;
+};
+
+template <int NI, int T, typename H>
+__device__ __forceinline__ Norm norm_of(const H (&v)[NI][4], int kind, float eps, int t, int D, double (*red)[T / 64], int& turn) {
+    Norm n = {0.0, 1.0};
+    if (kind == NORM_NONE) return n;
     double s = 0;
+    if (kind == NORM_LAYER) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s = fma(v[i][c], v[i][c], s);
-    const double inv = 1.0 / sqrt(row_sum<T>(s, red, turn) / D + eps);
+            for (int c = 0; c < 4; ++c) s += v[i][c];      // zeros past the row's end
+        n.mean = row_sum<T>(s, red, turn) / D;
+        s = 0;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e0 = 4 * (t + i * T);
-        f32x4 ww = {1, 1, 1, 1}, bb = {0, 0, 0, 0};
-        if (w) ww = load4<float, f32x4>((const char*)w, e0, D, vw);
-        if (b) bb = load4<float, f32x4>((const char*)b, e0, D, vb);
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[i][c] = v[i][c] * inv * ww[c] + bb[c];
+            for (int c = 0; c < 4; ++c) {
+                const double d = 4 * (t + i * T) + c < D ? v[i][c] - n.mean : 0.0;
+                s = fma(d, d, s);
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s = fma((double)v[i][c], (double)v[i][c], s);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    n.inv = 1.0 / sqrt(row_sum<T>(s, red, turn) / D + eps);
+    return n;
+}
+
+// out = (v - mean) / sqrt(..) * w + b; w 1 and b 0 without.  Values past the row's end get a weight of 0.
+template <int NI, int T, bool VEC, typename H, typename O>
+__device__ __forceinline__ void normed(O& out, H (&v)[NI][4], int kind, const float* w, const float* b, float eps, int t, int D, const Row<VEC>& wr,
+                                       const Row<VEC>& br, double (*red)[T / 64], int& turn) {
+    u32x4 ww[NI];
+    if (w) load_row<NI, T, VEC>(ww, wr, t, T_F32);
+    else
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ww[i][c] = 4 * (t + i * T) + c < D ? 0x3F800000u : 0u;
+    const Norm n = norm_of<NI, T>(v, kind, eps, t, D, red, turn);
+    afresh(v);
+    if (b) {
+        u32x4 bb[NI];
+        load_row<NI, T, VEC>(bb, br, t, T_F32);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                out[i][c] = (v[i][c] - n.mean) * n.inv * (double)__uint_as_float(ww[i][c]) + (double)__uint_as_float(bb[i][c]);
+    } else if (kind == NORM_LAYER) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) out[i][c] = (v[i][c] - n.mean) * n.inv * (double)__uint_as_float(ww[i][c]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {   // a group at a time, for the registers' sake
+#pragma unroll
+            for (int c = 0; c < 4; ++c) out[i][c] = v[i][c] * n.inv * (double)__uint_as_float(ww[i][c]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
 }
 
+// rint(x inv) within -127 .. 127; 0 where that is NaN (the conversion gives 0 for NaN and the ends of the range for
+// what passes them).
 __device__ __forceinline__ int code_of(float x, float inv) {
-    const float r = rintf(x * inv);
-    return r != r ? 0 : r > 127.f ? 127 : r < -127.f ? -127 : (int)r;
+    int q;
+    asm("v_cvt_i32_f32 %0, %1" : "=v"(q) : "v"(rintf(x * inv)));
+    return min(max(q, -127), 127);
 }
 
-// T threads a row, NI groups of 4 values a thread; 256 / T rows a workgroup below 256 threads.
-template <int T, int NI>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void k_block_norm(NormArgs a) {
+// T threads a row, NI groups of 4 values a thread; 256 / T rows a workgroup below 256 threads.  H: what the row is
+// held in, float where that loses nothing.  Values past the row's end are zeros or NaN (a norm of a row that is not
+// finite): neither counts in a sum that is, nor in the largest value or a code.
+template <int T, int NI, typename H, bool VEC>
+__global__ __launch_bounds__(T < 256 ? 256 : T, NI <= 2 ? 6 : NI <= 4 ? 4 : 3) void k_block_norm(NormArgs a) {
     __shared__ double red[2][T < 256 ? 1 : T / 64];
     static_assert(T == 64 || T >= 256, "a row has one wave or a whole workgroup");
     constexpr int ROWS = T < 256 ? 256 / T : 1;
-    const int64_t m = (int64_t)wide_index(blockIdx.y) * ROWS + threadIdx.x / T;
+    const int64_t m = (int64_t)wide_index(blockIdx.y) * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x / T);
     const int t = threadIdx.x % T, D = a.D;
     int64_t rows = a.M;
     if (a.used) rows = a.used[0] < rows ? a.used[0] : rows;
     if (m >= rows) return;   // a whole wave, or the whole workgroup where it shares the row
     int turn = 0;
     double (*scratch)[T / 64] = (double (*)[T / 64])red;
+    typedef Row<VEC> R;
 
-    double v[NI][4];
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[i][c] = 0.0;
+    u32x4 xr[NI], br[NI];
+    if (a.x) load_row<NI, T, VEC>(xr, R(a.x, m * a.ldx, D, type_bytes(a.x_type)), t, a.x_type);
+    if (a.b && !a.place) load_row<NI, T, VEC>(br, R(a.b, m * a.ldb, D, type_bytes(a.b_type)), t, a.b_type);
     f32x4 x[NI];
-    if (a.x) load_row<NI, T>(x, a.x + m * a.ldx * type_bytes(a.x_type), t, D, a.x_type, a.vec & V_X);
+    H v[NI][4];
     if (a.b) {
-        const int n = a.place ? a.parts : 1;
-        for (int j = 0; j < n; ++j) {
-            const int64_t from = a.place ? a.place[m * n + j] : m;
-            if ((uint64_t)from >= (uint64_t)a.b_rows) continue;
-            const double w = a.place && a.weight ? a.weight[m * n + j] : 1.0;
-            f32x4 b[NI];
-            load_row<NI, T>(b, a.b + from * a.ldb * type_bytes(a.b_type), t, D, a.b_type, a.vec & V_B);
+        if (sizeof(H) == 4 || !a.place) {   // a row held in fp32 comes from no sum, norm or gate
+            to_values(x, br, a.b_type);
 #pragma unroll
             for (int i = 0; i < NI; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[i][c] = fma(w, (double)b[i][c], v[i][c]);
-        }
-        norm_row<NI, T>(v, a.post, a.post_w, a.post_b, a.vec & V_POST_W, a.vec & V_POST_B, a.eps, t, D, scratch, turn);
-        if (a.gate) {
-            const char* g = (const char*)(a.gate + m * a.ld_gate);
+                for (int c = 0; c < 4; ++c) v[i][c] = x[i][c];
+        } else {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const f32x4 gg = load4<float, f32x4>(g, 4 * (t + i * T), D, a.vec & V_GATE);
+            for (int i = 0; i < NI; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[i][c] *= gg[c];
+                for (int c = 0; c < 4; ++c) v[i][c] = 0;
+            for (int j = 0; j < a.parts; ++j) {
+                const int64_t from = a.place[m * a.parts + j];
+                if ((uint64_t)from >= (uint64_t)a.b_rows) continue;
+                const double w = a.weight ? a.weight[m * a.parts + j] : 1.0;
+                load_row<NI, T, VEC>(br, R(a.b, from * a.ldb, D, type_bytes(a.b_type)), t, a.b_type);
+                to_values(x, br, a.b_type);
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[i][c] = (H)fma(w, (double)x[i][c], (double)v[i][c]);
             }
         }
-        const double bs = a.b_scale;
+        if (sizeof(H) == 8 && a.post != NORM_NONE)
+            normed<NI, T>(v, v, a.post, a.post_w, a.post_b, a.eps, t, D, R(a.post_w, 0, D, 4), R(a.post_b, 0, D, 4), scratch, turn);
+        if (sizeof(H) == 8 && a.gate) {
+            u32x4 g[NI];
+            load_row<NI, T, VEC>(g, R(a.gate, m * a.ld_gate, D, 4), t, T_F32);
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+            for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[i][c] *= bs;
+                for (int c = 0; c < 4; ++c) v[i][c] *= (H)values(g[i], T_F32)[c];
+        }
     }
-    if (a.x) {
-        const double xs = a.x_scale;
+    if (a.x) to_values(x, xr, a.x_type);
+    const double bs = a.b_scale, xs = a.x_scale;
+    if (a.b && a.x) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[i][c] = (H)fma(xs, (double)x[i][c], v[i][c] * bs);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    } else if (a.b) {
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[i][c] = fma(xs, (double)x[i][c], v[i][c]);
+            for (int c = 0; c < 4; ++c) v[i][c] = (H)(v[i][c] * bs);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[i][c] = (H)(xs * (double)x[i][c]);
     }
     if (a.xo) {
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[i][c] = x[i][c] = rounded((float)v[i][c], a.x_type);
-        store_row<NI, T>(x, a.xo + m * a.ldxo * type_bytes(a.x_type), t, D, a.x_type, a.vec & V_XO);
+            for (int c = 0; c < 4; ++c) x[i][c] = (float)v[i][c];
+        if (a.x_type == T_BF16) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) x[i] = __builtin_convertvector(__builtin_convertvector(x[i], bf16x4), f32x4);
+        } else if (a.x_type == T_F16) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) x[i] = __builtin_convertvector(__builtin_convertvector(x[i], f16x4), f32x4);
+        }
+        store_row<NI, T, VEC>(x, R(a.xo, m * a.ldxo, D, type_bytes(a.x_type)), t, a.x_type);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[i][c] = x[i][c];
     }
     if (!a.y && !a.xscale) return;
-    norm_row<NI, T>(v, a.pre, a.pre_w, a.pre_b, a.vec & V_PRE_W, a.vec & V_PRE_B, a.eps, t, D, scratch, turn);
+    if (a.pre == NORM_NONE) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[i][c] = 4 * (t + i * T) + c < D ? (float)v[i][c] : 0.f;
-    if (a.y) store_row<NI, T>(x, a.y + m * a.ldy * type_bytes(a.y_type), t, D, a.y_type, a.vec & V_Y);
+            for (int c = 0; c < 4; ++c) x[i][c] = (float)v[i][c];
+    } else {
+        normed<NI, T>(x, v, a.pre, a.pre_w, a.pre_b, a.eps, t, D, R(a.pre_w, 0, D, 4), R(a.pre_b, 0, D, 4), scratch, turn);
+    }
+    if (a.y) store_row<NI, T, VEC>(x, R(a.y, m * a.ldy, D, type_bytes(a.y_type)), t, a.y_type);
     if (!a.xscale) return;
 
     // INT8 rows
-    float most = 0.f;   // NaN compares false: skipped
+    float most = 0.f;   // the larger of a value and NaN is the value
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) most = fabsf(x[i][c]) > most ? fabsf(x[i][c]) : most;
+        for (int c = 0; c < 4; ++c) most = __builtin_fmaxf(most, __builtin_fabsf(x[i][c]));
 #pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) {
-        const float o = __shfl_xor(most, s, 64);
-        most = o > most ? o : most;
-    }
+    for (int s = 32; s >= 1; s >>= 1) most = fmaxf(most, __shfl_xor(most, s, 64));
     if (T > 64) {
         float* red_f = (float*)&scratch[turn][0];
         if ((threadIdx.x & 63) == 0) red_f[threadIdx.x >> 6] = most;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < T / 64; ++w) most = red_f[w] > most ? red_f[w] : most;
+        for (int w = 0; w < T / 64; ++w) most = fmaxf(most, red_f[w]);
         turn ^= 1;
     }
     const float inv = most > 0.f ? 1.f / most * 127.f : 0.f;   // a reciprocal and a product, each rounded
     if (t == 0) a.xscale[m] = most / 127.f;
-    int32_t sum = 0;
+    uint32_t word[NI];   // 4 codes each; 0 past the row's end
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        const int e0 = 4 * (t + i * T);
-        uint32_t word = 0;
+        int q[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int q = code_of(x[i][c], inv);   // 0 past the row's end
-            sum += q;
-            word |= ((uint32_t)q & 0xFFu) << (8 * c);
-        }
-        if (a.Xq && e0 < D) {
-            int8_t* o = a.Xq + m * a.ldXq + e0;
-            if ((a.vec & V_Q) && e0 + 4 <= D) *(uint32_t*)o = word;
-            else
+        for (int c = 0; c < 4; ++c) q[c] = code_of(x[i][c], inv);
+        word[i] = __builtin_amdgcn_perm((uint32_t)q[1], (uint32_t)q[0], 0x0C0C0400u) | __builtin_amdgcn_perm((uint32_t)q[3], (uint32_t)q[2], 0x04000C0Cu);
+    }
+    if (a.Xq) {
+        const R qr(a.Xq, m * a.ldXq, D, 1);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (e0 + c < D) o[c] = (int8_t)(word >> (8 * c));
-        }
-        if (a.Xb && 128 * ((t + i * T) / 32) < D) {   // whole groups of 32 lanes, 4 words: all of them are written, zeros included
+        for (int i = 0; i < NI; ++i) qr.store_bytes(4 * (t + i * T), word[i]);
+    }
+    if (a.Xb) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if (128 * ((t + i * T) / 32) >= D) continue;   // whole groups of 32 lanes, 4 words: all of them are written, zeros included
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
                 // bit p of the 4 bytes (no carries: the partial products are apart), then the 8 lanes of a word
-                const uint32_t nib = (((word >> p) & 0x01010101u) * 0x01020408u) >> 24;
+                const uint32_t nib = (((word[i] >> p) & 0x01010101u) * 0x01020408u) >> 24;
                 const uint32_t w = or_reduce8_to_last(nib << (4 * (t & 7)));
                 const int at = (t + i * T) >> 3;
                 if ((t & 7) == 7 && at < a.ldXb) a.Xb[(m * 8 + p) * a.ldXb + at] = w;
             }
         }
-    }
-    if (a.Xb) {   // words past those
+        // words past those
         const int done = (D + 127) / 128 * 4;
         for (int64_t i = t; i < 8 * (a.ldXb - done); i += T) a.Xb[(m * 8 + i / (a.ldXb - done)) * a.ldXb + done + i % (a.ldXb - done)] = 0u;
     }
     if (a.xsum) {
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) sum = __builtin_amdgcn_sdot4((int)word[i], 0x01010101, sum, false);
 #pragma unroll
         for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s, 64);
         if (T > 64) {
@@ -274,23 +409,42 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_block_norm(NormArgs a) {
     }
 }
 
+// Whether what is held of a row are fp32 numbers: one input as it is, or the stream rounded to x's type.
+bool narrow(const NormArgs& a) {
+    if (a.place || a.post != NORM_NONE || a.gate) return false;
+    return a.xo || (a.b ? !a.x && a.b_scale == 1.f : a.x_scale == 1.f);
+}
+
+// Whether every operand can be read or written 4 values at a time.
+bool by_four(const NormArgs& a) {
+    const auto has = [&](const void* p, uint32_t bit) { return !p || (a.vec & bit); };
+    return a.D % 4 == 0 && has(a.x, V_X) && has(a.b, V_B) && has(a.gate, V_GATE) && has(a.xo, V_XO) && has(a.y, V_Y) && has(a.Xq, V_Q) &&
+           has(a.post_w, V_POST_W) && has(a.post_b, V_POST_B) && has(a.pre_w, V_PRE_W) && has(a.pre_b, V_PRE_B);
+}
+
 template <int T, int NI>
 void go(const NormArgs& a, hipStream_t s) {
     constexpr int ROWS = T < 256 ? 256 / T : 1;
     const int64_t groups = (a.M + ROWS - 1) / ROWS;
-    hipLaunchKernelGGL((k_block_norm<T, NI>), dim3(wide(groups), parts(groups)), dim3(T < 256 ? 256 : T), 0, s, a);
+    const dim3 grid(wide(groups), parts(groups)), block(T < 256 ? 256 : T);
+    if (!by_four(a))    hipLaunchKernelGGL((k_block_norm<T, NI, double, false>), grid, block, 0, s, a);
+    else if (narrow(a)) hipLaunchKernelGGL((k_block_norm<T, NI, float, true>), grid, block, 0, s, a);
+    else                hipLaunchKernelGGL((k_block_norm<T, NI, double, true>), grid, block, 0, s, a);
 }
 
 }  // namespace
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
     const int groups = (a.D + 3) / 4;
+    // few threads a row, so that many rows are in flight (8192 rows of 4096: 79 us with 256 threads, 84 with 512,
+    // 184 with 1024), but registers for the row (16384 of 11008: 183 us with 512 threads, 271 with 768)
     if (groups <= 64) go<64, 1>(a, s);
     else if (groups <= 128) go<64, 2>(a, s);
     else if (groups <= 256) go<256, 1>(a, s);
     else if (groups <= 512) go<256, 2>(a, s);
     else if (groups <= 1024) go<256, 4>(a, s);
     else if (groups <= 2048) go<512, 4>(a, s);
+    else if (groups <= 6 * 512) go<512, 6>(a, s);
     else go<1024, 4>(a, s);
     return hipGetLastError();
 }

@@ -5,13 +5,14 @@
 //     D[p, n] = sum_k q[row(p), k] w_e[n, k]    (exact int32), then the epilogue
 //
 // Bound by the stream of weights (1 or 2 bits each).  A workgroup of 4 waves
-// has 16 columns (of both matrices, with a gate) and up to 16 MT positions of
-// one expert; the waves share k, chunk by chunk, so that even a narrow matrix
-// keeps every compute unit busy, and join their sums through LDS.  A
-// wave's load is 1 KiB of packed weights, its 64-k steps go through the int8
-// matrix cores with the weights as rows and the positions as columns: a lane
-// ends with 4 neighbouring outputs of one position.  The positions' rows come
-// through the caches.
+// has 16 F weight rows (half of each matrix with a gate) and up to 16 MT
+// positions of one expert; the waves share k, chunk by chunk, so that even a
+// narrow matrix keeps every compute unit busy, and join their sums through
+// LDS.  A wave's load is 1 KiB of packed weights; the loads of its next chunk
+// are in flight while it multiplies.  Weights are the rows of a matrix
+// instruction and positions its columns: a lane ends with 4 neighbouring
+// outputs of one position.  The positions' INT8 rows come through the caches,
+// once for F fragments.
 #include "expert_kernel.hpp"
 
 namespace bnn {
@@ -19,16 +20,17 @@ namespace {
 
 constexpr int WAVES = 4;
 
-template <bool TERN, bool GATED, int MT>
-__global__ __launch_bounds__(64 * WAVES) void k_expert_rows(ExpertArgs a, int frags, int chunks, int slots) {
-    constexpr int H = GATED ? 2 : 1, CK = chunk_k(TERN), STEPS = CK / 64;
-    __shared__ v4i part[WAVES][H * MT][64];
+template <bool TERN, bool GATED, int MT, int F>
+__global__ __launch_bounds__(64 * WAVES, MT * F > 4 ? 3 : 4) void k_expert_rows(ExpertArgs a, int frags, int chunks, int slots, uint32_t groups) {
+    constexpr int CK = chunk_k(TERN), STEPS = CK / 64, COLS = GATED ? F / 2 : F;   // fragments of columns
+    __shared__ v4i part[WAVES][F * MT][64];
     const uint32_t id = wide_index(blockIdx.y);
-    const int f = (int)(id / (uint32_t)slots), slot = (int)(id % (uint32_t)slots);
-    if (f >= frags) return;
+    if (id >= groups) return;
+    const int f0 = (int)(id / (uint32_t)slots) * COLS, slot = (int)(id % (uint32_t)slots);
     const Tile t = find_tile(a, slot, 16 * MT);
     if (t.e < 0) return;   // the same in the whole workgroup
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r16 = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     const int8_t* row[MT];
 #pragma unroll
@@ -36,83 +38,106 @@ __global__ __launch_bounds__(64 * WAVES) void k_expert_rows(ExpertArgs a, int fr
         const int src = source_row(a, t.p0 + min(16 * i + r16, t.n - 1));
         row[i] = a.Xq + (int64_t)max(src, 0) * a.ldXq;
     }
-    const int64_t at = ((int64_t)t.e * frags + f) * chunks * 64 + lane;
-    const uint4* w[2] = {a.m.W + at, GATED ? a.u.W + at : nullptr};
-    v4i acc[H][MT];
+    const uint4* w[F];
 #pragma unroll
-    for (int h = 0; h < H; ++h)
+    for (int q = 0; q < F; ++q)
+        w[q] = (GATED && q >= COLS ? a.u.W : a.m.W) + ((int64_t)t.e * frags + min(f0 + q % COLS, frags - 1)) * chunks * 64;
+    v4i acc[F][MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) acc[h][i] = v4i{0, 0, 0, 0};
+    for (int q = 0; q < F; ++q)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[q][i] = v4i{0, 0, 0, 0};
 
+    uint4 next[F];
+    const auto fetch = [&](int c) {
+        const int64_t to = (int64_t)min(c, chunks - 1) * 64;
+#pragma unroll
+        for (int q = 0; q < F; ++q) next[q] = (w[q] + to)[lane];
+    };
+    fetch(wave);
     for (int c = wave; c < chunks; c += WAVES) {
-        uint32_t bits[H][4];
+        uint32_t bits[F][4];
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const uint4 b = w[h][(int64_t)c * 64];
-            bits[h][0] = b.x; bits[h][1] = b.y; bits[h][2] = b.z; bits[h][3] = b.w;
-        }
+        for (int q = 0; q < F; ++q) { bits[q][0] = next[q].x; bits[q][1] = next[q].y; bits[q][2] = next[q].z; bits[q][3] = next[q].w; }
+        fetch(c + WAVES);
+        const auto step = [&](int s, const v4i (&x)[MT]) {
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int k = CK * c + 64 * s;
-            if (k < a.K) {
-                v4i x[MT];
+            for (int q = 0; q < F; ++q) {
+                const v4i b = expand16<TERN>(bits[q], s);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    if (k + 64 <= a.K) x[i] = *(const v4i*)(row[i] + k + 16 * g);
-                    else x[i] = masked16(row[i], k + 16 * g, a.K);
-                }
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    const v4i b = expand16<TERN>(bits[h], s);
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) acc[h][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b, x[i], acc[h][i], 0, 0, 0);
-                }
+                for (int i = 0; i < MT; ++i) acc[q][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b, x[i], acc[q][i], 0, 0, 0);
             }
+        };
+        const int k0 = CK * c + 16 * g;
+        if (CK * (c + 1) <= a.K) {
+            v4i x[STEPS][MT];
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) x[s][i] = *(const v4i*)(row[i] + k0 + 64 * s);
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) step(s, x[s]);
+        } else {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+                if (CK * c + 64 * s < a.K) {
+                    v4i x[MT];
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) x[i] = masked16(row[i], k0 + 64 * s, a.K);
+                    step(s, x);
+                }
         }
     }
 #pragma unroll
-    for (int h = 0; h < H; ++h)
+    for (int q = 0; q < F; ++q)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) part[wave][h * MT + i][lane] = acc[h][i];
+        for (int i = 0; i < MT; ++i) part[wave][q * MT + i][lane] = acc[q][i];
     __syncthreads();
-    for (int i = wave; i < MT; i += WAVES) {
-        const int in = 16 * i + r16;
-        if (in >= t.n) continue;
-        const int p = t.p0 + in, src = source_row(a, p), n = 16 * f + 4 * g;
-        if (src < 0 || n >= a.N) continue;
-        v4i d = part[0][i][lane], du = {0, 0, 0, 0};
+    for (int j = wave; j < COLS * MT; j += WAVES) {
+        const int q = j / MT, i = j % MT, in = 16 * i + r16, n = 16 * (f0 + q) + 4 * g;
+        if (in >= t.n || n >= a.N) continue;
+        const int p = t.p0 + in, src = source_row(a, p);
+        if (src < 0) continue;
+        v4i d = {0, 0, 0, 0}, du = {0, 0, 0, 0};
 #pragma unroll
-        for (int v = 1; v < WAVES; ++v) d += part[v][i][lane];
-        if (GATED)
-#pragma unroll
-            for (int v = 0; v < WAVES; ++v) du += part[v][(H - 1) * MT + i][lane];
+        for (int v = 0; v < WAVES; ++v) {
+            d += part[v][j][lane];
+            if (GATED) du += part[v][COLS * MT + j][lane];
+        }
         finish<GATED>(a, p, a.xscale ? a.xscale[src] : 1.f, n, d, du, scale4(a.m, t.e, n, a.N), GATED ? scale4(a.u, t.e, n, a.N) : Scale4{});
     }
 }
 
-int rows_tile(const ExpertArgs& a) {   // 16-row fragments of a tile, by the average of an expert's rows
-    const int64_t mean = a.positions / a.experts;
-    return mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
+int rows_tile(const ExpertArgs& a) { return a.positions / a.experts <= 16 ? 1 : 2; }   // 16-row fragments, by the average of an expert's rows
+
+int64_t groups_of(const ExpertArgs& a, int f) {
+    const int cols = 16 * (a.u.W ? f / 2 : f);
+    return tile_slots(a, 16 * rows_tile(a)) * ((a.N + cols - 1) / cols);
 }
 
-int64_t groups_of(const ExpertArgs& a) { return tile_slots(a, 16 * rows_tile(a)) * ((a.N + 15) / 16); }
+// Weight fragments of a wave: 4, to read the INT8 rows seldom (8 x 16 rows, 11008 -> 4096: 30 against 31 us, 8 x 8 rows,
+// 4096 -> 2 x 11008: 36 against 38), but 2 where that gives fewer than two workgroups to a compute unit (2 rows,
+// 11008 -> 4096: 7.7 against 9.3).
+int rows_frags(const ExpertArgs& a) { return groups_of(a, 4) >= 512 ? 4 : 2; }
 
 }  // namespace
 
-bool expert_rows_fits(const ExpertArgs& a, bool) { return groups_of(a) < ((int64_t)1 << 31); }
+bool expert_rows_fits(const ExpertArgs& a, bool) { return groups_of(a, 2) < ((int64_t)1 << 31); }
 
 hipError_t launch_expert_rows(const ExpertArgs& a, bool ternary, hipStream_t s) {
-    const int mt = rows_tile(a), frags = (a.N + 15) / 16, chunks = (a.K + chunk_k(ternary) - 1) / chunk_k(ternary);
+    const int mt = rows_tile(a), f = rows_frags(a), frags = (a.N + 15) / 16, chunks = (a.K + chunk_k(ternary) - 1) / chunk_k(ternary);
     const int slots = (int)tile_slots(a, 16 * mt);
-    const int64_t groups = groups_of(a);
+    const int64_t groups = groups_of(a, f);
     const dim3 grid(wide(groups), parts(groups)), block(64 * WAVES);
     const bool gated = a.u.W != nullptr;
-#define BNN_ROWS(T, G, MT) hipLaunchKernelGGL((k_expert_rows<T, G, MT>), grid, block, 0, s, a, frags, chunks, slots)
+#define BNN_ROWS(T, G, MT, F) hipLaunchKernelGGL((k_expert_rows<T, G, MT, F>), grid, block, 0, s, a, frags, chunks, slots, (uint32_t)groups)
+#define BNN_ROWS_F(T, G, MT) do { if (f == 4) BNN_ROWS(T, G, MT, 4); else BNN_ROWS(T, G, MT, 2); } while (0)
 #define BNN_ROWS_MT(T, G) \
-    do { if (mt == 1) BNN_ROWS(T, G, 1); else if (mt == 2) BNN_ROWS(T, G, 2); else BNN_ROWS(T, G, 4); } while (0)
+    do { if (mt == 1) BNN_ROWS_F(T, G, 1); else BNN_ROWS_F(T, G, 2); } while (0)
     if (ternary) { if (gated) BNN_ROWS_MT(true, true); else BNN_ROWS_MT(true, false); }
     else         { if (gated) BNN_ROWS_MT(false, true); else BNN_ROWS_MT(false, false); }
 #undef BNN_ROWS_MT
+#undef BNN_ROWS_F
 #undef BNN_ROWS
     return hipGetLastError();
 }

@@ -1,4 +1,4 @@
-// Grouped products with many rows to an expert: tiles of 64 to 256 positions x
+// Grouped products with many rows to an expert: tiles of 64 or 128 positions x
 // 256 weight rows (128 of each matrix with a gate) on the int8 matrix cores.
 //
 //     D[p, n] = sum_k q[row(p), k] w_e[n, k]    (exact int32), then the epilogue
@@ -6,12 +6,15 @@
 // Bound by the matrix cores and what feeds them.  Four waves share the tile by
 // weight rows: each has all its positions and 64 weight rows, so that every
 // weight is expanded by one wave only, in registers, straight from global
-// memory (a chunk of 256 or 512 k ahead), and serves 4 to 16 matrix
+// memory (a chunk of 256 or 512 k ahead), and serves 4 or 8 matrix
 // instructions.  Only the INT8 rows go through LDS: stages of 128 k, brought
 // by loads to LDS three stages ahead of their use (a ring of four), the
 // 16-byte pieces of a row permuted by the row so that the 8 lanes that are
-// served together fall on distinct banks.  LDS reads are 64 KiB a 64-k step
-// for 256 positions, half of what the matrix cores' time allows.  Weights are
+// served together fall on distinct banks.  LDS reads are 32 KiB a 64-k step
+// for 128 positions, half of what the matrix cores' time allows.  Two
+// workgroups share a compute unit, so that one's epilogue runs beside the
+// other's products (256 positions in one workgroup: 406 against 388 us for
+// 8192^3, 121 against 84 us for 2000 x 11008 -> 4096).  Weights are
 // the rows of an instruction and positions its columns: a lane ends with 4
 // neighbouring outputs of a position.
 //
@@ -25,6 +28,7 @@
 namespace bnn {
 namespace {
 
+constexpr int THREADS = 256;                // 4 waves
 constexpr int FN = 4;                       // weight fragments of a wave
 constexpr int ST = 128, RING = 4;           // k of a stage; stages in LDS
 
@@ -46,10 +50,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, uint
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
 }
 
-// RW waves share the positions, each with MF fragments of 16, and four the weight rows.
-template <bool TERN, bool GATED, int RW, int MF>
-__global__ __launch_bounds__(256 * RW, 2) void k_expert_tile(ExpertArgs a, int frags, int chunks, int tiles_n, uint32_t x_bytes) {
-    constexpr int THREADS = 256 * RW, BM = 16 * MF * RW, CK = chunk_k(TERN), CS = CK / ST;   // stages of a weight chunk
+// MF: fragments of 16 positions in a tile.
+template <bool TERN, bool GATED, int MF>
+__global__ __launch_bounds__(THREADS, 2) void k_expert_tile(ExpertArgs a, int frags, int chunks, int tiles_n, uint32_t x_bytes) {
+    constexpr int BM = 16 * MF, CK = chunk_k(TERN), CS = CK / ST;   // stages of a weight chunk
     constexpr int PIECES = BM * ST / 16 / THREADS;                  // 16-byte loads of a lane for a stage
     __shared__ __attribute__((aligned(16))) int8_t lds0[BM * ST], lds1[BM * ST], lds2[BM * ST], lds3[BM * ST];
     auto buf = [&](auto I) -> int8_t* {
@@ -62,7 +66,7 @@ __global__ __launch_bounds__(256 * RW, 2) void k_expert_tile(ExpertArgs a, int f
     __shared__ int source[BM];
     __shared__ float factor[BM];
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 3, wr = wave >> 2;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     // which tile
     const int slots = tile_count(a, BM);
@@ -108,7 +112,7 @@ __global__ __launch_bounds__(256 * RW, 2) void k_expert_tile(ExpertArgs a, int f
     const uint4* w[FN];
 #pragma unroll
     for (int q = 0; q < FN; ++q) {
-        const int f = GATED ? 8 * tn + 2 * wn + (q >> 1) : 16 * tn + 4 * wn + q;
+        const int f = GATED ? 8 * tn + 2 * wave + (q >> 1) : 16 * tn + 4 * wave + q;
         w[q] = (GATED && (q & 1) ? a.u.W : a.m.W) + ((int64_t)t.e * frags + min(f, frags - 1)) * chunks * 64;
     }
     uint32_t now[FN][4], next[FN][4];
@@ -128,7 +132,7 @@ __global__ __launch_bounds__(256 * RW, 2) void k_expert_tile(ExpertArgs a, int f
         for (int q = 0; q < FN; ++q) acc[i][q] = v4i{0, 0, 0, 0};
     int at[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) at[u] = (16 * MF * wr + r16) * ST + (((4 * u + g) ^ (r16 & 7)) << 4);
+    for (int u = 0; u < 2; ++u) at[u] = r16 * ST + (((4 * u + g) ^ (r16 & 7)) << 4);
 
     // The two 64-k steps of stage P of a chunk group.
     constexpr int AHEAD = 4;                   // row fragments that are read before their use
@@ -202,10 +206,10 @@ __global__ __launch_bounds__(256 * RW, 2) void k_expert_tile(ExpertArgs a, int f
         if (s + 3 < stages) stage(s + 3, Ic<3>{});
     }
 
-    // Epilogue.  The ring is free: each wave parks 32 columns of its sums at a time in a part of its own (16-byte
+    // Epilogue.  The ring is free: each wave parks 32 columns of its sums at a time in a buffer of its own (16-byte
     // pieces permuted by the row, as above) and reads them back row by row, so that neighbouring lanes store
     // neighbouring columns and the code for an output stands here once.
-    int8_t* mine = (wn == 0 ? lds0 : wn == 1 ? lds1 : wn == 2 ? lds2 : lds3) + 16 * MF * wr * 128;
+    int8_t* mine = wave == 0 ? lds0 : wave == 1 ? lds1 : wave == 2 ? lds2 : lds3;
 #pragma unroll
     for (int c = 0; c < FN / 2; ++c) {
         __syncthreads();
@@ -215,48 +219,51 @@ __global__ __launch_bounds__(256 * RW, 2) void k_expert_tile(ExpertArgs a, int f
             for (int h = 0; h < 2; ++h) *(v4i*)(mine + (16 * i + r16) * 128 + (((4 * h + g) ^ (r16 & 7)) << 4)) = acc[i][2 * c + h];
         __syncthreads();
         constexpr int LANES = GATED ? 4 : 8;          // of a row
-        const int f = GATED ? 8 * tn + 2 * wn + c : 16 * tn + 4 * wn + 2 * c;
+        const int f = GATED ? 8 * tn + 2 * wave + c : 16 * tn + 4 * wave + 2 * c;
         const int j = lane % LANES, n = 16 * f + 4 * j;
         if (n < a.N) {
             const Scale4 sm = scale4(a.m, t.e, n, a.N), su = GATED ? scale4(a.u, t.e, n, a.N) : Scale4{};
-            const int first_row = 16 * MF * wr, rows = min(16 * MF, t.n - first_row);
 #pragma unroll 1
-            for (int row = lane / LANES; row < rows; row += 64 / LANES) {
-                if (source[first_row + row] < 0) continue;
+            for (int row = lane / LANES; row < t.n; row += 64 / LANES) {
+                if (source[row] < 0) continue;
                 const int8_t* at_row = mine + row * 128;
                 const v4i d = *(const v4i*)(at_row + ((j ^ (row & 7)) << 4));
                 const v4i du = GATED ? *(const v4i*)(at_row + (((4 + j) ^ (row & 7)) << 4)) : v4i{0, 0, 0, 0};
-                finish<GATED>(a, t.p0 + first_row + row, factor[first_row + row], n, d, du, sm, su);
+                finish<GATED>(a, t.p0 + row, factor[row], n, d, du, sm, su);
             }
         }
     }
 }
 
-int tile_rows(const ExpertArgs& a) {
-    const int64_t mean = a.positions / a.experts;
-    return mean >= 192 ? 256 : mean >= 96 ? 128 : 64;
+int64_t tiles_of(const ExpertArgs& a, int rows) {
+    const int64_t cols = a.u.W ? 128 : 256;
+    return (tile_slots(a, rows) * ((a.N + cols - 1) / cols) + 7) / 8 * 8;
 }
 
-int64_t tiles_of(const ExpertArgs& a) {
-    const int64_t cols = a.u.W ? 128 : 256;
-    return (tile_slots(a, tile_rows(a)) * ((a.N + cols - 1) / cols) + 7) / 8 * 8;
-}
+// 128 positions where that gives two workgroups to each compute unit and an
+// expert has so many, otherwise 64 (8 x 2048 positions, 4096 -> 11008 with a
+// gate: 1353 against 1418 us; 8 x 256, 4096 -> 4096: 44 against 39).
+int tile_rows(const ExpertArgs& a) { return a.positions / a.experts >= 96 && tiles_of(a, 128) >= 512 ? 128 : 64; }
 
 }  // namespace
 
+// From 24 rows of an expert where the tiles give two workgroups to each
+// compute unit (8 x 32 rows, 4096 -> 2 x 11008: 48 against 62 us with
+// expert_rows.hip), from 40 always (8 x 32 rows, 11008 -> 4096, 128 tiles: 48
+// against 39; 8 x 48: 50 against 63).  Offsets into Xq are 32 bits here.
 bool expert_tile_takes(const ExpertArgs& a) {
-    return (int64_t)a.rows * a.ldXq < ((int64_t)1 << 31) && tiles_of(a) < ((int64_t)1 << 24) && a.positions / a.experts > 48;
+    const int64_t mean = a.positions / a.experts, tiles = tiles_of(a, 64);
+    return (mean > 40 || (mean >= 24 && tiles >= 512)) && (int64_t)a.rows * a.ldXq < ((int64_t)1 << 31) && tiles < ((int64_t)1 << 24);
 }
 
 hipError_t launch_expert_tile(const ExpertArgs& a, bool ternary, hipStream_t s) {
     const int cols = a.u.W ? 128 : 256, frags = (a.N + 15) / 16, chunks = (a.K + chunk_k(ternary) - 1) / chunk_k(ternary);
     const int tiles_n = (a.N + cols - 1) / cols, rows = tile_rows(a);
     const uint32_t x_bytes = (uint32_t)(a.rows * a.ldXq);
-    const dim3 grid((unsigned)tiles_of(a));
+    const dim3 grid((unsigned)tiles_of(a, rows)), block(THREADS);
     const bool gated = a.u.W != nullptr;
-#define BNN_TILE(T, G, RW, MF) hipLaunchKernelGGL((k_expert_tile<T, G, RW, MF>), grid, dim3(256 * RW), 0, s, a, frags, chunks, tiles_n, x_bytes)
-#define BNN_TILE_MF(T, G) \
-    do { if (rows == 256) BNN_TILE(T, G, 2, 8); else if (rows == 128) BNN_TILE(T, G, 1, 8); else BNN_TILE(T, G, 1, 4); } while (0)
+#define BNN_TILE(T, G, MF) hipLaunchKernelGGL((k_expert_tile<T, G, MF>), grid, block, 0, s, a, frags, chunks, tiles_n, x_bytes)
+#define BNN_TILE_MF(T, G) do { if (rows == 128) BNN_TILE(T, G, 8); else BNN_TILE(T, G, 4); } while (0)
     if (ternary) { if (gated) BNN_TILE_MF(true, true); else BNN_TILE_MF(true, false); }
     else         { if (gated) BNN_TILE_MF(false, true); else BNN_TILE_MF(false, false); }
 #undef BNN_TILE_MF

@@ -6,7 +6,7 @@
 //     order    the pairs of e at offsets[e] .., in their own order
 //
 // A wave owns a row: lane l holds the logits of experts l, l + 64, ..., and a
-// round of the choice is a butterfly maximum over (key, lowest index).  The
+// round of the choice is a maximum over the wave in registers and a ballot for the lowest index.  The
 // sort is a stable count: ranks within 64 neighbouring pairs by comparing the
 // experts' bits across the wave (a ballot a bit), the waves of a tile and the
 // tiles of a workgroup by counts in LDS, the workgroups by counts in the
@@ -23,27 +23,44 @@ constexpr int THREADS = 1024, WAVES = THREADS / 64;
 constexpr int MAX_PARTS = 256;       // workgroups that share the rows
 constexpr int ONE_PART_ROWS = 64;    // rows that one workgroup takes in one launch
 
-// Keys in the order of an unsigned integer; 0 for what is never chosen (-inf, NaN).
-__device__ __forceinline__ uint64_t key_of(float x) {
-    if (!(x > -__builtin_inff())) return 0;
+// Keys in the order of an unsigned integer, in two words; 0 for what is never
+// chosen (-inf, NaN), which no other value's first word is.
+struct Key {
+    uint32_t hi, lo;
+};
+__device__ __forceinline__ Key key_of(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);   // -0 as +0: they are equal
-    return (uint64_t)(u >> 31 ? ~u : u | 0x80000000u) << 32;
+    return {x > -__builtin_inff() ? (u >> 31 ? ~u : u | 0x80000000u) : 0u, 0u};
 }
-__device__ __forceinline__ uint64_t key_of(double x) {
-    if (!(x > -__builtin_inf())) return 0;
-    const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
-    return u >> 63 ? ~u : u | 0x8000000000000000ull;
+__device__ __forceinline__ Key key_of(double x) {
+    uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+    u = x > -__builtin_inf() ? (u >> 63 ? ~u : u | 0x8000000000000000ull) : 0ull;
+    return {(uint32_t)(u >> 32), (uint32_t)u};
+}
+
+// Over the wave, in registers (row shifts, then the rows' last lanes on to the next ones); the result is in lane 63.
+template <typename Op>
+__device__ __forceinline__ uint32_t wave_fold(uint32_t v, Op op) {   // 0 must change nothing
+#define BNN_FOLD(ctrl, rows) v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xF, false))
+    BNN_FOLD(0x111, 0xF);
+    BNN_FOLD(0x112, 0xF);
+    BNN_FOLD(0x114, 0xF);
+    BNN_FOLD(0x118, 0xF);
+    BNN_FOLD(0x142, 0xA);
+    BNN_FOLD(0x143, 0xC);
+#undef BNN_FOLD
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    return wave_fold(v, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    return __uint_as_float(wave_fold(__float_as_uint(v), [](uint32_t x, uint32_t y) { return __float_as_uint(__uint_as_float(x) + __uint_as_float(y)); }));
 }
 
 __device__ __forceinline__ float logit_at(const char* row, int e, int type) {
     if (type == T_F32) return ((const float*)row)[e];
     return type == T_BF16 ? (float)((const __bf16*)row)[e] : (float)((const _Float16*)row)[e];
-}
-
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) v = fmaxf(v, __shfl_xor(v, s, 64));
-    return v;
 }
 
 // The experts of one row, by one wave; each is also counted in `count` (LDS).
@@ -57,14 +74,16 @@ __device__ void choose(const RouteArgs& a, int row, int lane, uint32_t* count) {
         l[i] = e < a.experts ? logit_at(lr, e, a.type) : -__builtin_inff();
         if (l[i] != l[i]) l[i] = -__builtin_inff();
     }
-    uint64_t key[PER];
-    float most = -__builtin_inff(), total = 0.f;
-    if (!a.sigmoid) {
+    Key key[PER], plain[PER];
+    uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) most = fmaxf(most, l[i]);
-        most = wave_max(most);
-        if (most == -__builtin_inff()) most = 0.f;
+    for (int i = 0; i < PER; ++i) {
+        plain[i] = key_of(l[i]);
+        top = plain[i].hi > top ? plain[i].hi : top;
     }
+    top = wave_max(top);
+    const float most = top == 0 ? 0.f : __uint_as_float(top >> 31 ? top & 0x7FFFFFFFu : ~top);   // the largest logit
+    float total = 0.f;
     if (a.bias) {
         double s[PER], sum = 0;
 #pragma unroll
@@ -77,48 +96,49 @@ __device__ void choose(const RouteArgs& a, int row, int lane, uint32_t* count) {
         for (int i = 0; i < PER; ++i) {
             const int e = lane + 64 * i;
             const double v = a.sigmoid || sum == 0.0 ? s[i] : s[i] / sum;
-            key[i] = e < a.experts && l[i] > -__builtin_inff() ? key_of(v + (double)a.bias[e]) : 0;
+            key[i] = e < a.experts && l[i] > -__builtin_inff() ? key_of(v + (double)a.bias[e]) : Key{0, 0};
         }
         total = (float)sum;
     } else {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            key[i] = key_of(l[i]);
-            if (!a.sigmoid) total += expf(l[i] - most);
-        }
-        if (!a.sigmoid)
+        for (int i = 0; i < PER; ++i) key[i] = plain[i];
+        if (!a.sigmoid) {
 #pragma unroll
-            for (int s = 32; s >= 1; s >>= 1) total += __shfl_xor(total, s, 64);
+            for (int i = 0; i < PER; ++i) total += expf(l[i] - most);
+            total = wave_sum(total);
+        }
     }
     int mine = -1;   // lane j keeps choice j
     for (int j = 0; j < a.top; ++j) {
-        uint64_t best = 0;
-        int at = 0x7FFFFFFF;
+        uint32_t hi = 0, lo = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (key[i] > best) { best = key[i]; at = lane + 64 * i; }   // the lowest index first
+        for (int i = 0; i < PER; ++i) hi = key[i].hi > hi ? key[i].hi : hi;
+        hi = wave_max(hi);
+        if (hi == 0) break;   // the same in all lanes
+        if (a.bias) {
 #pragma unroll
-        for (int s = 32; s >= 1; s >>= 1) {
-            const uint64_t k = __shfl_xor((unsigned long long)best, s, 64);
-            const int e = __shfl_xor(at, s, 64);
-            if (k > best || (k == best && e < at)) { best = k; at = e; }
+            for (int i = 0; i < PER; ++i) lo = key[i].hi == hi && key[i].lo > lo ? key[i].lo : lo;
+            lo = wave_max(lo);
         }
-        if (best == 0) break;   // the same in all lanes
+        int at = -1;   // the lowest index that has the largest key
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i) {
+            const uint64_t has = __ballot(key[i].hi == hi && key[i].lo == lo);
+            at = has ? 64 * i + __ffsll((unsigned long long)has) - 1 : at;
+        }
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (at == lane + 64 * i) key[i] = 0;
+            if (at == lane + 64 * i) key[i].hi = 0;
         if (lane == j) mine = at;
     }
     float w = 0.f;
     if (mine >= 0) {
-        float lg = logit_at(lr, mine, a.type);
+        const float lg = logit_at(lr, mine, a.type);
         w = a.sigmoid ? 1.f / (1.f + expf(-lg)) : expf(lg - most) / total;
-        if (count) atomicAdd(&count[mine], 1u);
+        atomicAdd(&count[mine], 1u);
     }
     if (a.renorm) {
-        float sum = w;
-#pragma unroll
-        for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s, 64);
+        const float sum = wave_sum(w);
         w = sum == 0.f ? 0.f : w / sum;
     }
     if (lane < a.top) {
@@ -240,13 +260,32 @@ __global__ __launch_bounds__(THREADS) void k_route_place(RouteArgs a) {
     __shared__ uint32_t base[2 * MAX_EXPERTS], red[WAVES];
     __shared__ uint16_t part[WAVES][MAX_EXPERTS];
     const int tid = threadIdx.x, rows = used_rows(a);
-    uint32_t mine = 0, before = 0;
-    if (tid < a.experts)
-        for (int g = 0; g < (int)gridDim.x; ++g) {
-            const uint32_t n = (uint32_t)a.work[(int64_t)g * a.experts + tid];
-            if (g < (int)blockIdx.x) before += n;
-            mine += n;
+    // pairs of each expert in all workgroups and in those before this one: a slice of the workgroups to each group of
+    // threads as long as the experts, 8 counts in flight
+    __shared__ uint32_t sums[2][MAX_EXPERTS];
+    if (tid < a.experts) sums[0][tid] = sums[1][tid] = 0;
+    __syncthreads();
+    const int slices = THREADS / a.experts, slice = tid / a.experts, e = tid - slice * a.experts;
+    if (slice < slices) {
+        uint32_t own = 0, ahead = 0;
+        for (int g = slice; g < (int)gridDim.x; g += 8 * slices) {
+            uint32_t n[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int h = g + u * slices;
+                n[u] = h < (int)gridDim.x ? (uint32_t)a.work[(int64_t)h * a.experts + e] : 0u;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                own += n[u];
+                if (g + u * slices < (int)blockIdx.x) ahead += n[u];
+            }
         }
+        atomicAdd(&sums[0][e], own);   // whole numbers: in any order the same
+        atomicAdd(&sums[1][e], ahead);
+    }
+    __syncthreads();
+    const uint32_t mine = tid < a.experts ? sums[0][tid] : 0, before = tid < a.experts ? sums[1][tid] : 0;
     uint32_t all;
     const uint32_t at = scan_experts(mine, red, all);
     if (tid < a.experts) {
