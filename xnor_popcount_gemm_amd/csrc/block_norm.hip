@@ -156,15 +156,14 @@ __device__ __forceinline__ void afresh(H (&v)[NI][4]) {
             for (int c = 0; c < 4; ++c) asm volatile("" : "+v"(v[i][c]));
 }
 
-// What a norm takes off and multiplies with.
+// What the norm of factor * v takes off v and multiplies it with.
 struct Norm {
     double mean, inv;
 };
 
 template <int NI, int T, typename H>
-__device__ __forceinline__ Norm norm_of(const H (&v)[NI][4], int kind, float eps, int t, int D, double (*red)[T / 64], int& turn) {
-    Norm n = {0.0, 1.0};
-    if (kind == NORM_NONE) return n;
+__device__ __forceinline__ Norm norm_of(const H (&v)[NI][4], int kind, double factor, float eps, int t, int D, double (*red)[T / 64], int& turn) {
+    Norm n = {0.0, factor};
     double s = 0;
     if (kind == NORM_LAYER) {
 #pragma unroll
@@ -188,13 +187,13 @@ __device__ __forceinline__ Norm norm_of(const H (&v)[NI][4], int kind, float eps
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    n.inv = 1.0 / sqrt(row_sum<T>(s, red, turn) / D + eps);
+    n.inv = factor / sqrt(factor * factor * (row_sum<T>(s, red, turn) / D) + eps);
     return n;
 }
 
-// out = (v - mean) / sqrt(..) * w + b; w 1 and b 0 without.  Values past the row's end get a weight of 0.
+// out = the norm of factor * v, with w and b; 1 and 0 without.  Values past the row's end get a weight of 0.
 template <int NI, int T, bool VEC, typename H, typename O>
-__device__ __forceinline__ void normed(O& out, H (&v)[NI][4], int kind, const float* w, const float* b, float eps, int t, int D, const Row<VEC>& wr,
+__device__ __forceinline__ void normed(O& out, H (&v)[NI][4], int kind, double factor, const float* w, const float* b, float eps, int t, int D, const Row<VEC>& wr,
                                        const Row<VEC>& br, double (*red)[T / 64], int& turn) {
     u32x4 ww[NI];
     if (w) load_row<NI, T, VEC>(ww, wr, t, T_F32);
@@ -203,7 +202,7 @@ __device__ __forceinline__ void normed(O& out, H (&v)[NI][4], int kind, const fl
         for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) ww[i][c] = 4 * (t + i * T) + c < D ? 0x3F800000u : 0u;
-    const Norm n = norm_of<NI, T>(v, kind, eps, t, D, red, turn);
+    const Norm n = norm_of<NI, T>(v, kind, factor, eps, t, D, red, turn);
     afresh(v);
     if (b) {
         u32x4 bb[NI];
@@ -283,7 +282,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, NI <= 2 ? 6 : NI <= 4 ? 4 : 3) v
             }
         }
         if (sizeof(H) == 8 && a.post != NORM_NONE)
-            normed<NI, T>(v, v, a.post, a.post_w, a.post_b, a.eps, t, D, R(a.post_w, 0, D, 4), R(a.post_b, 0, D, 4), scratch, turn);
+            normed<NI, T>(v, v, a.post, 1.0, a.post_w, a.post_b, a.eps, t, D, R(a.post_w, 0, D, 4), R(a.post_b, 0, D, 4), scratch, turn);
         if (sizeof(H) == 8 && a.gate) {
             u32x4 g[NI];
             load_row<NI, T, VEC>(g, R(a.gate, m * a.ld_gate, D, 4), t, T_F32);
@@ -295,7 +294,24 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, NI <= 2 ? 6 : NI <= 4 ? 4 : 3) v
     }
     if (a.x) to_values(x, xr, a.x_type);
     const double bs = a.b_scale, xs = a.x_scale;
-    if (a.b && a.x) {
+    double factor = 1.0;   // the stream is factor * v
+    if (sizeof(H) == 4 && !a.xo) {
+        // one input as it is, its factor left to the norm
+        factor = a.x ? xs : bs;
+        if (a.x) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[i][c] = x[i][c];
+        }
+    } else if (sizeof(H) == 4 && a.b && a.x && bs == 1.0 && xs == 1.0) {
+        // a sum of two fp32 numbers rounded once (through 64 bits it is the same: 53 >= 2 * 24 + 2), without conversions to
+        // 64 bits, which take four times as long as the operations
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[i][c] = (H)((float)x[i][c] + (float)v[i][c]);
+    } else if (a.b && a.x) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
 #pragma unroll
@@ -336,9 +352,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, NI <= 2 ? 6 : NI <= 4 ? 4 : 3) v
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) x[i][c] = (float)v[i][c];
+            for (int c = 0; c < 4; ++c) x[i][c] = (float)(v[i][c] * factor);
     } else {
-        normed<NI, T>(x, v, a.pre, a.pre_w, a.pre_b, a.eps, t, D, R(a.pre_w, 0, D, 4), R(a.pre_b, 0, D, 4), scratch, turn);
+        normed<NI, T>(x, v, a.pre, factor, a.pre_w, a.pre_b, a.eps, t, D, R(a.pre_w, 0, D, 4), R(a.pre_b, 0, D, 4), scratch, turn);
     }
     if (a.y) store_row<NI, T, VEC>(x, R(a.y, m * a.ldy, D, type_bytes(a.y_type)), t, a.y_type);
     if (!a.xscale) return;
@@ -412,7 +428,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, NI <= 2 ? 6 : NI <= 4 ? 4 : 3) v
 // Whether what is held of a row are fp32 numbers: one input as it is, or the stream rounded to x's type.
 bool narrow(const NormArgs& a) {
     if (a.place || a.post != NORM_NONE || a.gate) return false;
-    return a.xo || (a.b ? !a.x && a.b_scale == 1.f : a.x_scale == 1.f);
+    return a.xo || !a.b || !a.x;
 }
 
 // Whether every operand can be read or written 4 values at a time.

@@ -20,8 +20,8 @@ namespace {
 
 constexpr int MAX_EXPERTS = 1024;
 constexpr int THREADS = 1024, WAVES = THREADS / 64;
-constexpr int MAX_PARTS = 256;       // workgroups that share the rows
-constexpr int ONE_PART_ROWS = 64;    // rows that one workgroup takes in one launch
+constexpr int MAX_PARTS = 256;       // workgroups that share the rows, 16 or more to each
+constexpr int ONE_PART_ROWS = 32;    // rows that one workgroup takes in one launch
 
 // Keys in the order of an unsigned integer, in two words; 0 for what is never
 // chosen (-inf, NaN), which no other value's first word is.
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(THREADS) void k_route_place(RouteArgs a) {
 
 int route_parts(int64_t rows) {
     if (rows <= ONE_PART_ROWS) return 1;
-    const int64_t n = (rows + ONE_PART_ROWS - 1) / ONE_PART_ROWS;
+    const int64_t n = (rows + WAVES - 1) / WAVES;
     return (int)(n < MAX_PARTS ? n : MAX_PARTS);
 }
 
