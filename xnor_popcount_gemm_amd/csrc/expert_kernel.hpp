@@ -126,10 +126,15 @@ __device__ __forceinline__ float activate(float z, int act) {
     }
 }
 
+// Whether the 4 values from p on, column n, can be read or written together.
+template <typename E>
+__device__ __forceinline__ bool together(const E* p, int n, int N) { return n + 4 <= N && (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(E) - 1)) == 0; }
+
 // alpha[n .. n+3] and the like of expert e; entries past N are not read.
 __device__ __forceinline__ f32x4 row4(const float* p, int64_t ld, int e, int n, int N) {
     const float* q = p + (int64_t)e * ld + n;
     f32x4 v = {0, 0, 0, 0};
+    if (together(q, n, N)) return *(const f32x4*)q;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (n + i < N) v[i] = q[i];
@@ -163,12 +168,14 @@ __device__ __forceinline__ void finish4(const ExpertArgs& a, int p, int n, f32x4
     typedef E e4 __attribute__((ext_vector_type(4)));
     if (a.r) {
         const E* r = (const E*)a.r + (int64_t)p * a.ldr + n;
+        if (together(r, n, a.N)) v = v + __builtin_convertvector(*(const e4*)r, f32x4);
+        else
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < a.N) v[i] += (float)r[i];
+            for (int i = 0; i < 4; ++i)
+                if (n + i < a.N) v[i] += (float)r[i];
     }
     E* y = (E*)a.y + (int64_t)p * a.ldy + n;
-    if (n + 4 <= a.N && (reinterpret_cast<uintptr_t>(y) & (4 * sizeof(E) - 1)) == 0) {
+    if (together(y, n, a.N)) {
         *(e4*)y = __builtin_convertvector(v, e4);
     } else {
 #pragma unroll

@@ -52,7 +52,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, uint
 
 // MF: fragments of 16 positions in a tile.
 template <bool TERN, bool GATED, int MF>
-__global__ __launch_bounds__(THREADS, 2) void k_expert_tile(ExpertArgs a, int frags, int chunks, int tiles_n, uint32_t x_bytes) {
+__global__ __launch_bounds__(THREADS, MF == 4 ? 3 : 2) void k_expert_tile(ExpertArgs a, int frags, int chunks, int tiles_n, uint32_t x_bytes) {
     constexpr int BM = 16 * MF, CK = chunk_k(TERN), CS = CK / ST;   // stages of a weight chunk
     constexpr int PIECES = BM * ST / 16 / THREADS;                  // 16-byte loads of a lane for a stage
     __shared__ __attribute__((aligned(16))) int8_t lds0[BM * ST], lds1[BM * ST], lds2[BM * ST], lds3[BM * ST];
