@@ -1011,7 +1011,7 @@ def _float_type(t: torch.Tensor, name: str) -> int:
 
 def _matrix(t: torch.Tensor, dtype, name: str, rows: int, cols: int, index: int):
     """Address and row stride of a [rows, cols] matrix on device `index`."""
-    if not (t.dtype is dtype and t.get_device() == index and t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols):
+    if not (t.dtype is dtype and t.shape == (rows, cols) and t.get_device() == index):
         _dev(t, dtype, name)
         raise ValueError(f"{name} must be [{rows}, {cols}] on cuda:{index} (got {tuple(t.shape)} on {t.device})")
     row, col = t.stride()
@@ -1024,15 +1024,18 @@ def _vector(t: torch.Tensor | None, dtype, name: str, n: int, index: int) -> int
     """Address of a vector of n elements on device `index`; 0 for None."""
     if t is None:
         return 0
-    if t.get_device() != index:
+    if not (t.dtype is dtype and t.numel() == n and t.get_device() == index and t.is_contiguous()):
         _dev(t, dtype, name)
-        raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
-    return _flat(t, dtype, name, n)
+        raise ValueError(f"{name} must be contiguous on cuda:{index}, with {n} elements (got {tuple(t.shape)} on {t.device})")
+    return t.data_ptr() or _EMPTY
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _on(index: int, call, *args) -> int:
     """The status of a call that launches on device `index`, on its current stream."""
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         return call(*args, _raw_stream(index))
     with torch.cuda.device(index):
         return call(*args, _raw_stream(index))

@@ -4,7 +4,7 @@
 //
 //     D[p, n] = sum_k q[row(p), k] w_e[n, k]    (exact int32), then the epilogue
 //
-// Bound by the stream of weights (1 or 2 bits each).  A workgroup of 4 waves
+// Bound by the stream of weights (1 or 2 bits each).  A workgroup of 4 or 8 waves
 // has 16 F weight rows (half of each matrix with a gate) and up to 16 MT
 // positions of one expert; the waves share k, chunk by chunk, so that even a
 // narrow matrix keeps every compute unit busy, and join their sums through
@@ -18,15 +18,21 @@
 namespace bnn {
 namespace {
 
-constexpr int WAVES = 4;
+// Waves that share k: more where there are few workgroups (2 rows, 11008 -> 4096: 9.4 against 12.2 us), not otherwise
+// (8 x 8 rows, 4096 -> 2 x 11008: 72 against 55).
+constexpr int waves_of(int f) { return f == 2 ? 8 : 4; }
 
 template <bool TERN, bool GATED, int MT, int F>
-__global__ __launch_bounds__(64 * WAVES, MT * F > 4 ? 3 : 4) void k_expert_rows(ExpertArgs a, int frags, int chunks, int slots, uint32_t groups) {
-    constexpr int CK = chunk_k(TERN), STEPS = CK / 64, COLS = GATED ? F / 2 : F;   // fragments of columns
+__global__ __launch_bounds__(64 * waves_of(F), MT * F > 4 ? 3 : 4) void k_expert_rows(ExpertArgs a, int frags, int chunks) {
+    constexpr int WAVES = waves_of(F), CK = chunk_k(TERN), STEPS = CK / 64, COLS = GATED ? F / 2 : F;   // fragments of columns
     __shared__ v4i part[WAVES][F * MT][64];
-    const uint32_t id = wide_index(blockIdx.y);
-    if (id >= groups) return;
-    const int f0 = (int)(id / (uint32_t)slots) * COLS, slot = (int)(id % (uint32_t)slots);
+    // The tiles that there are, not those that there could be, to neighbouring workgroups: with gaps between them some
+    // compute units had twice as many as others (8 x 16 rows,
+    // 11008 -> 4096, 8 of 15 possible tiles, weights in the last-level cache: 30 against 20 us).
+    const uint32_t id = wide_index(blockIdx.y), slots = (uint32_t)tile_count(a, 16 * MT);
+    if (slots == 0) return;
+    const int f0 = (int)(id / slots) * COLS, slot = (int)(id % slots);
+    if (f0 >= frags) return;
     const Tile t = find_tile(a, slot, 16 * MT);
     if (t.e < 0) return;   // the same in the whole workgroup
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
@@ -55,6 +61,18 @@ __global__ __launch_bounds__(64 * WAVES, MT * F > 4 ? 3 : 4) void k_expert_rows(
         for (int q = 0; q < F; ++q) next[q] = (w[q] + to)[lane];
     };
     fetch(wave);
+    // the rows of the next chunk that lies within K, too, where they take few registers
+    constexpr bool EARLY = STEPS * MT <= 4;
+    v4i ahead[STEPS][MT];
+    const int whole = a.K / CK;
+    const auto load_rows = [&](v4i (&to)[STEPS][MT], int c) {
+        const int k = CK * min(c, whole - 1) + 16 * g;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) to[s][i] = *(const v4i*)(row[i] + k + 64 * s);
+    };
+    if (EARLY && whole > 0) load_rows(ahead, wave);
     for (int c = wave; c < chunks; c += WAVES) {
         uint32_t bits[F][4];
 #pragma unroll
@@ -69,12 +87,17 @@ __global__ __launch_bounds__(64 * WAVES, MT * F > 4 ? 3 : 4) void k_expert_rows(
             }
         };
         const int k0 = CK * c + 16 * g;
-        if (CK * (c + 1) <= a.K) {
+        if (c < whole) {
             v4i x[STEPS][MT];
+            if (EARLY) {
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s)
+                for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-                for (int i = 0; i < MT; ++i) x[s][i] = *(const v4i*)(row[i] + k0 + 64 * s);
+                    for (int i = 0; i < MT; ++i) x[s][i] = ahead[s][i];
+                load_rows(ahead, c + WAVES);
+            } else {
+                load_rows(x, c);
+            }
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) step(s, x[s]);
         } else {
@@ -108,16 +131,17 @@ __global__ __launch_bounds__(64 * WAVES, MT * F > 4 ? 3 : 4) void k_expert_rows(
     }
 }
 
-int rows_tile(const ExpertArgs& a) { return a.positions / a.experts <= 16 ? 1 : 2; }   // 16-row fragments, by the average of an expert's rows
+// 16-row fragments of a tile, by the average of an expert's rows: with 16 on average many an expert has more, and reads
+// its weights twice (8 experts, 128 rows in uneven shares, 11008 -> 4096: 27 us with 1, 24 with 2; 64 rows: 18 and 19).
+int rows_tile(const ExpertArgs& a) { return a.positions / a.experts <= 12 ? 1 : 2; }
 
 int64_t groups_of(const ExpertArgs& a, int f) {
     const int cols = 16 * (a.u.W ? f / 2 : f);
     return tile_slots(a, 16 * rows_tile(a)) * ((a.N + cols - 1) / cols);
 }
 
-// Weight fragments of a wave: 4, to read the INT8 rows seldom (8 x 16 rows, 11008 -> 4096: 30 against 31 us, 8 x 8 rows,
-// 4096 -> 2 x 11008: 36 against 38), but 2 where that gives fewer than two workgroups to a compute unit (2 rows,
-// 11008 -> 4096: 7.7 against 9.3).
+// Weight fragments of a wave: 4, to read the INT8 rows seldom (8 x 16 rows, 11008 -> 4096: 20 against 26 us), but 2 where
+// that gives fewer than two workgroups to a compute unit (2 rows, 11008 -> 4096: 7.7 against 9.3).
 int rows_frags(const ExpertArgs& a) { return groups_of(a, 4) >= 512 ? 4 : 2; }
 
 }  // namespace
@@ -126,11 +150,10 @@ bool expert_rows_fits(const ExpertArgs& a, bool) { return groups_of(a, 2) < ((in
 
 hipError_t launch_expert_rows(const ExpertArgs& a, bool ternary, hipStream_t s) {
     const int mt = rows_tile(a), f = rows_frags(a), frags = (a.N + 15) / 16, chunks = (a.K + chunk_k(ternary) - 1) / chunk_k(ternary);
-    const int slots = (int)tile_slots(a, 16 * mt);
     const int64_t groups = groups_of(a, f);
-    const dim3 grid(wide(groups), parts(groups)), block(64 * WAVES);
+    const dim3 grid(wide(groups), parts(groups)), block(64 * waves_of(f));
     const bool gated = a.u.W != nullptr;
-#define BNN_ROWS(T, G, MT, F) hipLaunchKernelGGL((k_expert_rows<T, G, MT, F>), grid, block, 0, s, a, frags, chunks, slots, (uint32_t)groups)
+#define BNN_ROWS(T, G, MT, F) hipLaunchKernelGGL((k_expert_rows<T, G, MT, F>), grid, block, 0, s, a, frags, chunks)
 #define BNN_ROWS_F(T, G, MT) do { if (f == 4) BNN_ROWS(T, G, MT, 4); else BNN_ROWS(T, G, MT, 2); } while (0)
 #define BNN_ROWS_MT(T, G) \
     do { if (mt == 1) BNN_ROWS_F(T, G, 1); else BNN_ROWS_F(T, G, 2); } while (0)
