@@ -564,3 +564,147 @@ def test_graph_replays(bnn, rows):
         torch.cuda.synchronize()
         for k in want:
             assert torch.equal(held[k][:n], want[k]), (i, k)
+
+
+# ---- the calls again, where they are most likely to go wrong
+
+
+@pytest.mark.parametrize("which", ["x", "branch"])
+@pytest.mark.parametrize("factor", [0.5, -3.0, 0.3, 0.0])
+@pytest.mark.parametrize("pre", ["none", "rms", "layer"])
+def test_norm_factor_of_one_input(bnn, which, factor, pre):
+    rng = np.random.default_rng(21)
+    banner(f"norm factor {which} {factor} {pre}")
+    for D in (256, 4096, 1001):
+        t = make(rng, (4, D), torch.bfloat16)
+        kw = dict(x_scale=factor) if which == "x" else dict(branch_scale=factor)
+        check_norm(bnn, t if which == "x" else None, t if which == "branch" else None, pre=pre, what=f"{which} {factor} {pre} {D}", **kw)
+
+
+def test_norm_stream_without_branch(bnn):
+    """x_out where only one input is given: the stream is stored and the norm reads it as stored."""
+    rng = np.random.default_rng(22)
+    banner("norm x_out of one input")
+    for D in (512, 777):
+        for kind in (torch.bfloat16, torch.float16, torch.float32):
+            x = make(rng, (5, D), kind)
+            out = {"x": torch.empty_like(x), "y": torch.empty((5, D), device="cuda")}
+            bnn.block_norm(x, x_scale=0.3, pre="rms", out=out)
+            torch.cuda.synchronize()
+            s, stored, v = ref.block_norm(x, None, x_scale=0.3)
+            np.testing.assert_array_equal(ref.f64(out["x"]), stored)
+            near(out["y"], v, ref.E32 * np.abs(v) + 1e-9, torch.float32, "y")
+            out = {"x": torch.empty((5, D), dtype=kind, device="cuda")}
+            bnn.block_norm(None, x, branch_scale=0.7, out=out)           # the branch alone, nothing but the stream asked for
+            torch.cuda.synchronize()
+            assert torch.equal(out["x"], (x.double() * float(np.float32(0.7))).float().to(kind))
+
+
+def test_norm_rows_far_apart(bnn):
+    """Rows past 2^32 bytes."""
+    rng = np.random.default_rng(23)
+    banner("norm rows far apart")
+    M, ld, D = 40000, 1 << 16, 136
+    big = torch.empty((M, ld), dtype=torch.bfloat16, device="cuda")
+    x = big[:, 64: 64 + D]
+    x.copy_(make(rng, (M, D), torch.bfloat16))
+    got = bnn.block_norm(x, y_dtype=torch.float32)
+    torch.cuda.synchronize()
+    at = np.r_[0:3, M - 3: M]
+    _, _, v = ref.block_norm(x[at.tolist()], None)
+    near(got["y"][at.tolist()], v, ref.E32 * np.abs(v) + 1e-9, torch.float32, "y")
+
+
+@pytest.mark.parametrize("K", [896, 1024, 1152, 1280, 1536, 2048, 4096, 5000])
+@pytest.mark.parametrize("ternary", [True, False])
+def test_linear_long_rows(bnn, K, ternary):
+    """Rows of many stages: every turn of the ring and of the weight chunks."""
+    rng = np.random.default_rng(K)
+    for P, N in ((70, 260), (300, 40), (1100, 130)):
+        check_linear(bnn, rng, 2, P, N, K, ternary=ternary, gated=N == 130, act="silu" if N == 130 else "none")
+
+
+def test_linear_wide_grids(bnn):
+    """128 positions to a tile: enough tiles for two workgroups to each compute unit."""
+    rng = np.random.default_rng(24)
+    check_linear(bnn, rng, 4, 3000, 6200, 200, ternary=True, how="even")
+    check_linear(bnn, rng, 3, 4100, 4100, 140, ternary=False, gated=True, act="relu2", out="bf16", how="ragged", rows=900, top=5)
+
+
+def test_linear_far_rows(bnn):
+    """Rows of INT8 values past 2^31 bytes, outputs past 2^32."""
+    rng = np.random.default_rng(25)
+    K, R, N = 200, 20000, 48
+    big = torch.zeros((R, 1 << 17), dtype=torch.int8, device="cuda")
+    rows = torch.tensor([0, 5, 16383, 16384, 19998, 19999])
+    big[rows.cuda(), :K] = torch.from_numpy(rng.integers(-127, 128, (6, K)).astype(np.int8)).cuda()
+    t, alpha, b, W = matrices(bnn, rng, 1, N, K, True, True, False)
+    for P in (6, 300):
+        order = rows[torch.arange(P) % 6].to(torch.int32)
+        out = torch.empty((P, 1 << 24), dtype=torch.bfloat16, device="cuda")[:, :N]
+        banner(f"far rows {P}")
+        bnn.expert_linear(big[:, :K], W, order=order.cuda(), out=out)
+        torch.cuda.synchronize()
+        want, off, _ = ref.expert_linear(big[rows.cuda()][:, :K], t, alpha, order=np.arange(P) % 6)
+        near(out, want, off, torch.bfloat16, f"far rows {P}")
+
+
+@pytest.mark.parametrize("P", [20, 400])
+def test_linear_offsets_past_the_positions(bnn, P):
+    """Offsets below 0 and past the positions count as the ends; one that decreases gives its expert no positions."""
+    rng = np.random.default_rng(26)
+    t, alpha, b, W = matrices(bnn, rng, 3, 40, 96, True, True, False)
+    Xq = int8_rows(bnn, rng, P, 96)
+    banner(f"offsets {P}")
+    for raw, clean in (([-5, P // 2, P // 2, P + 100], [0, P // 2, P // 2, P]), ([0, P, P // 3, P // 3], [0, P, P, P])):
+        y = torch.full((P, 40), LEFT, dtype=torch.float32, device="cuda")
+        bnn.expert_linear(Xq, W, offsets=torch.tensor(raw, dtype=torch.int32).cuda(), out=y)
+        torch.cuda.synchronize()
+        want, off, live = ref.expert_linear(Xq, t, alpha, offsets=clean)
+        near(y, want, off, torch.float32, str(raw))
+
+
+def test_two_streams_at_once(bnn):
+    rng = np.random.default_rng(27)
+    m = Experts(bnn, rng)
+    x = [make(rng, (257, 192)) for _ in range(2)]
+    used = torch.tensor([257], dtype=torch.int32).cuda()
+    banner("two streams")
+    want = [m(a, a, used)[-1]["y"].clone() for a in x]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for s, a in zip(streams, x):
+            with torch.cuda.stream(s):
+                got.append(m(a, a, used)[-1]["y"])
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_empty_calls(bnn):
+    banner("empty calls")
+    z = torch.empty((0, 64), device="cuda")
+    assert bnn.block_norm(z, z, y_dtype=torch.bfloat16, planes=True)["y"].shape == (0, 64)
+    r = bnn.expert_route(torch.empty((0, 8), device="cuda"), 2)
+    torch.cuda.synchronize()
+    assert r["offsets"].tolist() == [0] * 9
+    W = bnn.ExpertWeights(torch.zeros((3, 4), dtype=torch.int32, device="cuda"), 100, alpha=torch.ones(1, device="cuda"))
+    y = bnn.expert_linear(torch.empty((0, 112), dtype=torch.int8, device="cuda")[:, :100], W)
+    assert y.shape == (0, 3)
+
+
+def test_binding_checks(bnn):
+    """Wrong shapes, types and devices are refused before a launch."""
+    x, h = torch.zeros((4, 32), device="cuda"), torch.zeros((4, 32))
+    W = bnn.ExpertWeights(torch.zeros((3, 4), dtype=torch.int32, device="cuda"), 32, alpha=torch.ones(1, device="cuda"))
+    q = torch.zeros((4, 32), dtype=torch.int8, device="cuda")
+    for call in (lambda: bnn.block_norm(x, h), lambda: bnn.block_norm(x, torch.zeros((4, 31), device="cuda")), lambda: bnn.block_norm(x.double()),
+                 lambda: bnn.block_norm(x, pre="batch"), lambda: bnn.block_norm(x, pre_weight=torch.ones(31, device="cuda")), lambda: bnn.block_norm(x, weight=x),
+                 lambda: bnn.block_norm(x.T), lambda: bnn.block_norm(x, out={"y": torch.zeros((3, 32), device="cuda")}),
+                 lambda: bnn.expert_route(x, 2, score="tanh"), lambda: bnn.expert_route(x, 2, bias=torch.zeros(5, device="cuda")), lambda: bnn.expert_route(x, 33),
+                 lambda: bnn.expert_linear(q, W, act="tanh"), lambda: bnn.expert_linear(q.cpu(), W), lambda: bnn.expert_linear(x, W),
+                 lambda: bnn.expert_linear(q, W, xscale=torch.ones(3, device="cuda")), lambda: bnn.expert_linear(q, W, residual=torch.zeros((4, 3))),
+                 lambda: bnn.expert_linear(q, W, offsets=torch.zeros(3, dtype=torch.int32, device="cuda")), lambda: bnn.expert_linear(q, W, out_dtype=torch.float64)):
+        with pytest.raises((ValueError, TypeError, bnn.BnnError)):
+            call()

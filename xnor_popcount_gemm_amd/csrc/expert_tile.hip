@@ -38,12 +38,12 @@ typedef __attribute__((address_space(3))) void* lptr_t;
 template <int I> using Ic = std::integral_constant<int, I>;
 
 // s_waitcnt that leaves at most n vector-memory operations outstanding (vmcnt
-// in bits 3:0 and 15:14) and does not wait for the other counters.
-constexpr unsigned vmcnt(int n) { return (unsigned)(n & 0xF) | ((unsigned)((n >> 4) & 3) << 14) | (0x7u << 4) | (0xFu << 8); }
+// in bits 3:0 and 15:14) and no LDS access (lgkmcnt, bits 11:8).
+constexpr unsigned vmcnt(int n) { return (unsigned)(n & 0xF) | ((unsigned)((n >> 4) & 3) << 14) | (0x7u << 4); }
 
 // A barrier without the fence of __syncthreads(), which would wait for every
 // load to LDS in flight.  The caller has waited for its loads that the others
-// read next, and what it read from LDS has gone into matrix instructions.
+// read next, and for its own reads of the buffer that is filled next.
 __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, uint32_t bytes) {
@@ -161,28 +161,35 @@ __global__ __launch_bounds__(THREADS, MF == 4 ? 3 : 2) void k_expert_tile(Expert
         if (s < full) issue(I, s);
         else if (s < stages) issue_last(I, s);
     };
-    fetch(0);
-    issue_any(Ic<0>{}, 0);
-    issue_any(Ic<1>{}, 1);
-    issue_any(Ic<2>{}, 2);
     auto turn_chunk = [&](int s) INLINE {
 #pragma unroll
         for (int q = 0; q < FN; ++q)
 #pragma unroll
-            for (int d = 0; d < 4; ++d) now[q][d] = next[q][d];
+            for (int d = 0; d < 4; ++d) {
+                now[q][d] = next[q][d];
+                asm volatile("" : "+v"(now[q][d]));   // not expanded, and waited for, a stage earlier
+            }
         fetch(s / CS + 1);
     };
-    // A stage whose loads, and those that it starts, lie within the rows: its
-    // own are there when those of the two stages after it, and of the weights
-    // that were asked for since, are outstanding.
+    // A stage whose loads, and those that it starts, lie within the rows.  A
+    // stage asks for weights (every CS stages), then for rows, so its own rows,
+    // asked for three stages ago, are there when at most the rows of the next
+    // two stages are outstanding, and the weights asked for in the last two.
     auto fast_stage = [&](int s, auto P) INLINE {
         constexpr int p = decltype(P)::value;
-        constexpr int asked = (p + 3) % CS == 0 || (CS == 4 && (p + 2) % CS == 0) || CS == 2 ? FN : 0;
+        constexpr int asked = (p + CS - 1) % CS == 0 || (p + CS - 2) % CS == 0 ? FN : 0;
         __builtin_amdgcn_s_waitcnt(vmcnt(2 * PIECES + asked));
         barrier();
+        // With 64 positions the order is given (17 against 18.5 us for 64 experts; left free it also spills); with 128 it
+        // is left to the compiler (2 x 11008 x 4096: 1325 against 1350 us).
         if constexpr (p % CS == 0) turn_chunk(s);
+        if constexpr (MF == 4) {
+            __builtin_amdgcn_sched_barrier(0);
+            compute(P);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         issue(Ic<p + 3>{}, s + 3);
-        compute(P);
+        if constexpr (MF != 4) compute(P);
     };
     auto stage = [&](int s, auto P) INLINE {
         constexpr int p = decltype(P)::value;
@@ -193,11 +200,27 @@ __global__ __launch_bounds__(THREADS, MF == 4 ? 3 : 2) void k_expert_tile(Expert
         compute(P);
     };
     int s = 0;
-    for (; s + 6 < full; s += 4) {
-        fast_stage(s, Ic<0>{});
-        fast_stage(s + 1, Ic<1>{});
-        fast_stage(s + 2, Ic<2>{});
-        fast_stage(s + 3, Ic<3>{});
+    if (s + 6 < full) {
+        // the order of these loads is counted on: keep it
+        issue(Ic<0>{}, 0);
+        asm volatile("" ::: "memory");
+        fetch(0);
+        asm volatile("" ::: "memory");
+        issue(Ic<1>{}, 1);
+        asm volatile("" ::: "memory");
+        issue(Ic<2>{}, 2);
+        do {
+            fast_stage(s, Ic<0>{});
+            fast_stage(s + 1, Ic<1>{});
+            fast_stage(s + 2, Ic<2>{});
+            fast_stage(s + 3, Ic<3>{});
+            s += 4;
+        } while (s + 6 < full);
+    } else {
+        fetch(0);
+        issue_any(Ic<0>{}, 0);
+        issue_any(Ic<1>{}, 1);
+        issue_any(Ic<2>{}, 2);
     }
     for (; s < stages; s += 4) {
         stage(s, Ic<0>{});
