@@ -112,15 +112,22 @@ __device__ __forceinline__ int source_row(const ExpertArgs& a, int p) {
 
 enum : int32_t { ACT_NONE = 0, ACT_RELU = 1, ACT_RELU2 = 2, ACT_SILU = 3, ACT_GELU = 4, ACT_GELU_TANH = 5 };
 
+// z / (1 + exp(-t)) by the hardware's exponential and reciprocal, an ulp each: vector operations and matrix instructions
+// take turns on a SIMD, and at 2 x 11008 x 4096 the epilogue's took an eighth of the time with expf and a division.  The
+// exponential of a rounded argument is off by |t| 2^-24 of its value, as expf's would be.
+__device__ __forceinline__ float sigmoid_times(float z, float t) {
+    return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * t));
+}
+
 __device__ __forceinline__ float activate(float z, int act) {
     switch (act) {
     case ACT_RELU: return z < 0.f ? 0.f : z;   // NaN stays
     case ACT_RELU2: return z < 0.f ? 0.f : z * z;
-    case ACT_SILU: return z / (1.f + expf(-z));
+    case ACT_SILU: return sigmoid_times(z, z);
     case ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
     case ACT_GELU_TANH: {
         const float t = 1.5957691216057308f * (z + 0.044715f * z * z * z);   // 1 + tanh(t / 2) = 2 / (1 + exp(-t))
-        return z / (1.f + expf(-t));
+        return sigmoid_times(z, t);
     }
     default: return z;
     }
