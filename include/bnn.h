@@ -698,8 +698,7 @@ typedef struct bnn_norm_args {
  * Everything up to y is computed in 64 bits, s is rounded to x's type where
  * x_out is given (pre then reads the rounded stream, as a call of its own on
  * x_out would) and y to fp32; 16-bit outputs are rounded from fp32.  The
- * 64 bits cost nothing beside the memory traffic and make codes and scales the
- * same whatever the order of the sums.  A row's norms are over its D values;
+ * 64 bits make codes and scales the same whatever the order of the sums.  A row's norms are over its D values;
  * without x or branch their term is left out.  At least one output must be
  * given. */
 bnn_status bnn_block_norm(const bnn_norm_args* args, bnn_stream_t stream);
@@ -737,7 +736,8 @@ typedef struct bnn_route_args {
  * The pairs (row, choice) of an expert, in order of row * top + choice, take
  * the positions offsets[e] .. offsets[e+1]-1: order[position] = row * top +
  * choice and place[row, choice] = position.  Entries of order from
- * offsets[experts] on are left alone. */
+ * offsets[experts] on are left alone.  Calls that overlap in time need
+ * workspaces of their own; its contents need not be kept or cleared. */
 bnn_status bnn_expert_route(const bnn_route_args* args, bnn_stream_t stream);
 
 /* Workspace bytes of bnn_expert_route (0 where it uses none); -1 for sizes

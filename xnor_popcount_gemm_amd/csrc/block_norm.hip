@@ -8,10 +8,10 @@
 // Bound by memory traffic: each value is read once, held in registers through
 // its three or four row sums, and written once.  All arithmetic up to fl32(y)
 // is in 64 bits, so codes and scales do not depend on the order of a sum; that
-// costs about 10 of the 25 operations of a value.  8192 rows of 4096, fp32 stream + two
-// experts' rows -> stream, codes: 111 us, 5.1 TB/s, what a plain copy reaches;
-// one branch 79 us, 5.5 TB/s; 16384 rows of 11008 bfloat16 -> codes, 3 bytes
-// a value: 183 us, 3.0 TB/s, where the operations bound it.
+// costs about 10 of the 25 operations of a value.  8192 rows of 4096, fp32
+// stream + two experts' rows -> stream, output, codes: 124 us, 5.15 TB/s, what a plain
+// copy reaches; 16384 rows of 11008 bfloat16 -> codes, 3 bytes a value: 153 us,
+// 3.5 TB/s, where the operations bound it; one row: 6.7 us, its three sums.
 //
 // A row belongs to T threads (a wave, or up to 16 waves of a workgroup),
 // thread t holds the 4-value groups t, t + T, ... of it.  Rows are read and
@@ -453,7 +453,7 @@ void go(const NormArgs& a, hipStream_t s) {
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
     const int groups = (a.D + 3) / 4;
     // few threads a row, so that many rows are in flight (8192 rows of 4096: 79 us with 256 threads, 84 with 512,
-    // 184 with 1024), but registers for the row (16384 of 11008: 183 us with 512 threads, 271 with 768)
+    // 184 with 1024), but registers for the row (16384 of 11008: 183 us with 512 threads, 271 with 768, at that stage)
     if (groups <= 64) go<64, 1>(a, s);
     else if (groups <= 128) go<64, 2>(a, s);
     else if (groups <= 256) go<256, 1>(a, s);

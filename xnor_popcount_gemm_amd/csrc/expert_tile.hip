@@ -21,6 +21,11 @@
 // Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous run of the
 // tiles, in groups of 8 position tiles by weight tile, so that what is in its
 // L2 is used again.
+//
+// 8192^3 ternary: 391 us, 2811 TOPS (a library's int8 product 2082).  16384
+// positions of 8 experts, 4096 -> 2 x 11008 with a gate: 1262 us, 2340 TOPS:
+// matrix instructions take 57% of the cycles and vector instructions, which a
+// SIMD does not issue beside them, 34%.
 #include <type_traits>
 
 #include "expert_kernel.hpp"

@@ -6,12 +6,17 @@
 //     order    the pairs of e at offsets[e] .., in their own order
 //
 // A wave owns a row: lane l holds the logits of experts l, l + 64, ..., and a
-// round of the choice is a maximum over the wave in registers and a ballot for the lowest index.  The
-// sort is a stable count: ranks within 64 neighbouring pairs by comparing the
+// round of the choice is a maximum over the wave in registers and a ballot for
+// the lowest index.  The sort is a stable count: ranks within 64 neighbouring pairs by comparing the
 // experts' bits across the wave (a ballot a bit), the waves of a tile and the
 // tiles of a workgroup by counts in LDS, the workgroups by counts in the
 // workspace.  No atomic decides a position, so the order is the same on every
 // run.  A few rows are chosen and sorted by one workgroup in one launch.
+//
+// Bound by latency for few rows (1 x 8: 5.3 us, 200 x 64 with a bias: 7.4 and
+// 5.4 in two kernels), by the rounds of the choice for many (16384 x 128, 8 of
+// them: 18.6, and 8.3 for counts and places; 99 us in all with butterflies over
+// 64-bit keys and a thread that walked the workgroups' counts one by one).
 #include "bnn_device.hpp"
 #include "ffn.hpp"
 
