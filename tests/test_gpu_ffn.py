@@ -701,7 +701,8 @@ def test_binding_checks(bnn):
     q = torch.zeros((4, 32), dtype=torch.int8, device="cuda")
     for call in (lambda: bnn.block_norm(x, h), lambda: bnn.block_norm(x, torch.zeros((4, 31), device="cuda")), lambda: bnn.block_norm(x.double()),
                  lambda: bnn.block_norm(x, pre="batch"), lambda: bnn.block_norm(x, pre_weight=torch.ones(31, device="cuda")), lambda: bnn.block_norm(x, weight=x),
-                 lambda: bnn.block_norm(x.T), lambda: bnn.block_norm(x, out={"y": torch.zeros((3, 32), device="cuda")}),
+                 lambda: bnn.block_norm(x.T), lambda: bnn.block_norm(x, out={"Y": x}), lambda: bnn.block_norm(x, x, place=torch.zeros((2, 2), dtype=torch.int32, device="cuda")),
+                 lambda: bnn.block_norm(x, x, place=torch.zeros((4, 2), dtype=torch.int32, device="cuda"), weight=torch.ones((2, 4), device="cuda")), lambda: bnn.block_norm(x, out={"y": torch.zeros((3, 32), device="cuda")}),
                  lambda: bnn.expert_route(x, 2, score="tanh"), lambda: bnn.expert_route(x, 2, bias=torch.zeros(5, device="cuda")), lambda: bnn.expert_route(x, 33),
                  lambda: bnn.expert_linear(q, W, act="tanh"), lambda: bnn.expert_linear(q.cpu(), W), lambda: bnn.expert_linear(x, W),
                  lambda: bnn.expert_linear(q, W, xscale=torch.ones(3, device="cuda")), lambda: bnn.expert_linear(q, W, residual=torch.zeros((4, 3))),

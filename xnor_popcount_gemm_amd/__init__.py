@@ -30,7 +30,7 @@ __all__ = [
     "W_TERNARY", "pack_weights_ternary", "EPI_SIGN_PACK", "pack_activations_rsign", "conv3x3_fused",
     "KVCache", "qk_norm_rope", "rope_turns", "tree_mask", "tree_attention", "tree_attention_workspace",
     "cache_score_add", "cache_evict", "cache_evict_workspace",
-    "block_norm", "expert_route", "expert_route_workspace", "ExpertWeights", "expert_linear",
+    "block_norm", "expert_route", "expert_route_workspace", "ExpertWeights", "expert_linear", "MAX_NORM_D", "MAX_EXPERTS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbnn.so")
@@ -992,6 +992,7 @@ NORMS = {"none": 0, "rms": 1, "layer": 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+_NORM_OUT = {"x", "y", "Xq", "Xb", "xsum", "xscale"}
 MAX_NORM_D = 16384
 MAX_EXPERTS = 1024
 
@@ -1085,6 +1086,8 @@ def block_norm(x: torch.Tensor | None = None, branch: torch.Tensor | None = None
             out["xsum"] = torch.empty(M, dtype=torch.int32, device=dev)
         if int8 or planes:
             out["xscale"] = torch.empty(M, dtype=torch.float32, device=dev)
+    elif not out.keys() <= _NORM_OUT:
+        raise ValueError(f"out may hold {sorted(_NORM_OUT)} (got {sorted(out)})")
     get = out.get
     xo, y, Xq, Xb, xsum, xscale = get("x"), get("y"), get("Xq"), get("Xb"), get("xsum"), get("xscale")
     xp, bp, op, yp, qp, gp = (0, 0), (0, 0), (0, 0), (0, 0), (0, 0), (0, 0)
@@ -1112,6 +1115,8 @@ def block_norm(x: torch.Tensor | None = None, branch: torch.Tensor | None = None
             raise ValueError(f"out['Xb'] must be [{M}, 8, ld] on cuda:{index}")
         bits = Xb.data_ptr() or _EMPTY, _planes_ld(Xb)
     if place is not None:
+        if place.dim() != 2 or place.shape[0] != M or (weight is not None and weight.shape != place.shape):
+            raise ValueError(f"place and weight must be [{M}, parts] alike")
         parts = place.shape[1]
     elif weight is not None:
         raise ValueError("weight goes with place")

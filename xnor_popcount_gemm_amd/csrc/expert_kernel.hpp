@@ -39,60 +39,74 @@ __device__ __forceinline__ v4i masked16(const int8_t* row, int k, int K) {
     return v;
 }
 
-// Tile `slot` of the positions cut into tiles of `size` within each expert:
-// expert (-1: there are no so many tiles), first position, positions.  Every lane of the
-// wave calls it.
+// The positions cut into tiles of `size` within each expert.  Every lane of the
+// wave calls its functions; the offsets of the first 64 experts are read once.
 struct Tile {
-    int e, p0, n;
+    int e, p0, n;   // expert (-1: there are not so many tiles), first position, positions
 };
 
-__device__ __forceinline__ Tile find_tile(const ExpertArgs& a, int slot, int size) {
-    if (!a.offsets) {
-        const int p0 = slot * size;
-        return p0 < a.positions ? Tile{0, p0, min(size, a.positions - p0)} : Tile{-1, 0, 0};
-    }
-    const int lane = threadIdx.x & 63;
-    int before = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 64) {
-        const int e = e0 + lane;
-        int lo = 0, hi = 0;
+class Tiles {
+    // Lane l: positions lo .. hi-1 of expert e0 + l, their tiles, and the tiles up to and with them.
+    struct Span {
+        int lo, hi, n, sum;
+    };
+
+    __device__ __forceinline__ Span span(int e0) const {
+        const int lane = threadIdx.x & 63, e = e0 + lane;
+        Span s = {0, 0, 0, 0};
         if (e < a.experts) {   // offsets out of order or range give no positions
-            lo = max(a.offsets[e], 0);
-            hi = min(a.offsets[e + 1], a.positions);
+            s.lo = max(a.offsets[e], 0);
+            s.hi = min(a.offsets[e + 1], a.positions);
         }
-        const int n = hi > lo ? (hi - lo + size - 1) / size : 0;
-        int sum = n;
+        s.sum = s.n = s.hi > s.lo ? (s.hi - s.lo + size - 1) / size : 0;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d, 64);
-            if (lane >= d) sum += o;
+            const int o = __shfl_up(s.sum, d, 64);
+            if (lane >= d) s.sum += o;
         }
-        const uint64_t past = __ballot(before + sum > slot);
-        if (past) {
-            const int at = __ffsll((unsigned long long)past) - 1;
-            const int i = slot - before - __shfl(sum - n, at, 64), end = __shfl(hi, at, 64);
-            const int64_t p0 = __shfl(lo, at, 64) + (int64_t)i * size;
-            if (i < 0 || p0 >= end) return {-1, 0, 0};   // offsets that decrease
-            return {__builtin_amdgcn_readfirstlane(e0 + at), __builtin_amdgcn_readfirstlane((int)p0),
-                    __builtin_amdgcn_readfirstlane(min(size, end - (int)p0))};
-        }
-        before += __shfl(sum, 63, 64);
+        return s;
     }
-    return {-1, 0, 0};
-}
 
-// How many tiles of `size` the offsets make.  Every lane of the wave calls it.
-__device__ __forceinline__ int tile_count(const ExpertArgs& a, int size) {
-    if (!a.offsets) return (a.positions + size - 1) / size;
-    int sum = 0;
-    for (int e = threadIdx.x & 63; e < a.experts; e += 64) {
-        const int lo = max(a.offsets[e], 0), hi = min(a.offsets[e + 1], a.positions);
-        sum += hi > lo ? (hi - lo + size - 1) / size : 0;
+    const ExpertArgs& a;
+    const int size;
+    Span first;
+
+public:
+    __device__ __forceinline__ Tiles(const ExpertArgs& args, int tile) : a(args), size(tile), first{0, 0, 0, 0} {
+        if (a.offsets) first = span(0);
     }
-#pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s, 64);
-    return __builtin_amdgcn_readfirstlane(sum);
-}
+
+    __device__ __forceinline__ int count() const {
+        if (!a.offsets) return (a.positions + size - 1) / size;
+        int all = __shfl(first.sum, 63, 64);
+        for (int e0 = 64; e0 < a.experts; e0 += 64) all += __shfl(span(e0).sum, 63, 64);
+        return __builtin_amdgcn_readfirstlane(all);
+    }
+
+    __device__ __forceinline__ Tile operator[](int slot) const {
+        if (!a.offsets) {
+            const int p0 = slot * size;
+            return p0 < a.positions ? Tile{0, p0, min(size, a.positions - p0)} : Tile{-1, 0, 0};
+        }
+        int before = 0;
+        Span s = first;
+        for (int e0 = 0;;) {
+            const uint64_t past = __ballot(before + s.sum > slot);
+            if (past) {
+                const int at = __ffsll((unsigned long long)past) - 1;
+                const int i = slot - before - __shfl(s.sum - s.n, at, 64), end = __shfl(s.hi, at, 64);
+                const int64_t p0 = __shfl(s.lo, at, 64) + (int64_t)i * size;
+                if (i < 0 || p0 >= end) return {-1, 0, 0};   // offsets that decrease
+                return {__builtin_amdgcn_readfirstlane(e0 + at), __builtin_amdgcn_readfirstlane((int)p0),
+                        __builtin_amdgcn_readfirstlane(min(size, end - (int)p0))};
+            }
+            before += __shfl(s.sum, 63, 64);
+            e0 += 64;
+            if (e0 >= a.experts) return {-1, 0, 0};
+            s = span(e0);
+        }
+    }
+};
 
 // Tiles that cover any offsets.
 inline int64_t tile_slots(const ExpertArgs& a, int64_t size) {

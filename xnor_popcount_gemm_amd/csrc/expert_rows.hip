@@ -16,7 +16,7 @@
 //
 // 8 experts, 128 rows in uneven shares, 11008 -> 4096, weights from memory:
 // 28-33 us, 3 TB/s (from the last-level cache 18-24); 2 rows, 4096 -> 2 x
-// 11008: 13 us, 3.5 TB/s, a third of it the lookups before the stream.
+// 11008: 12.4 us, 3.6 TB/s, a third of it the lookups before the stream.
 #include "expert_kernel.hpp"
 
 namespace bnn {
@@ -33,21 +33,16 @@ __global__ __launch_bounds__(64 * waves_of(F), MT * F > 4 ? 3 : 4) void k_expert
     // The tiles that there are, not those that there could be, to neighbouring workgroups: with gaps between them some
     // compute units had twice as many as others (8 x 16 rows,
     // 11008 -> 4096, 8 of 15 possible tiles, weights in the last-level cache: 30 against 20 us).
-    const uint32_t id = wide_index(blockIdx.y), slots = (uint32_t)tile_count(a, 16 * MT);
+    const Tiles tiles(a, 16 * MT);
+    const uint32_t id = wide_index(blockIdx.y), slots = (uint32_t)tiles.count();
     if (slots == 0) return;
     const int f0 = (int)(id / slots) * COLS, slot = (int)(id % slots);
     if (f0 >= frags) return;
-    const Tile t = find_tile(a, slot, 16 * MT);
+    const Tile t = tiles[slot];
     if (t.e < 0) return;   // the same in the whole workgroup
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    const int8_t* row[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int src = source_row(a, t.p0 + min(16 * i + r16, t.n - 1));
-        row[i] = a.Xq + (int64_t)max(src, 0) * a.ldXq;
-    }
     const uint4* w[F];
 #pragma unroll
     for (int q = 0; q < F; ++q)
@@ -64,7 +59,13 @@ __global__ __launch_bounds__(64 * waves_of(F), MT * F > 4 ? 3 : 4) void k_expert
 #pragma unroll
         for (int q = 0; q < F; ++q) next[q] = (w[q] + to)[lane];
     };
-    fetch(wave);
+    fetch(wave);   // on its way while the rows are looked up
+    const int8_t* row[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int src = source_row(a, t.p0 + min(16 * i + r16, t.n - 1));
+        row[i] = a.Xq + (int64_t)max(src, 0) * a.ldXq;
+    }
     // the rows of the next chunk that lies within K, too, where they take few registers
     constexpr bool EARLY = STEPS * MT <= 4;
     v4i ahead[STEPS][MT];

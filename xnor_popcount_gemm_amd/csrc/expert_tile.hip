@@ -23,7 +23,7 @@
 // L2 is used again.
 //
 // 8192^3 ternary: 391 us, 2811 TOPS (a library's int8 product 2082).  16384
-// positions of 8 experts, 4096 -> 2 x 11008 with a gate: 1262 us, 2340 TOPS:
+// positions of 8 experts, 4096 -> 2 x 11008 with a gate: 1232-1262 us, 2340-2400 TOPS:
 // matrix instructions take 57% of the cycles and vector instructions, which a
 // SIMD does not issue beside them, 34%.
 #include <type_traits>
@@ -74,13 +74,14 @@ __global__ __launch_bounds__(THREADS, MF == 4 ? 3 : 2) void k_expert_tile(Expert
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     // which tile
-    const int slots = tile_count(a, BM);
+    const Tiles tiles(a, BM);
+    const int slots = tiles.count();
     const int total = slots * tiles_n, run = (total + 7) / 8;
     const int place = (int)(blockIdx.x >> 3), tile = (int)(blockIdx.x & 7) * run + place;
     if (place >= run || tile >= total) return;
     constexpr int GROUP = 8;
     const int grp = tile / (GROUP * tiles_n), first = grp * GROUP, size = min(slots - first, GROUP), in = tile - first * tiles_n;
-    const Tile t = find_tile(a, first + in % size, BM);
+    const Tile t = tiles[first + in % size];
     if (t.e < 0) return;
     const int tn = in / size;
 
