@@ -17,6 +17,7 @@
 // 8 experts, 128 rows in uneven shares, 11008 -> 4096, weights from memory:
 // 28-33 us, 3 TB/s (from the last-level cache 18-24); 2 rows, 4096 -> 2 x
 // 11008: 12.4 us, 3.6 TB/s, a third of it the lookups before the stream.
+#include "bnn_device.hpp"
 #include "expert_kernel.hpp"
 
 namespace bnn {
@@ -53,11 +54,16 @@ __global__ __launch_bounds__(64 * waves_of(F), MT * F > 4 ? 3 : 4) void k_expert
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[q][i] = v4i{0, 0, 0, 0};
 
-    uint4 next[F];
+    u32x4 next[F];
     const auto fetch = [&](int c) {
         const int64_t to = (int64_t)min(c, chunks - 1) * 64;
 #pragma unroll
-        for (int q = 0; q < F; ++q) next[q] = (w[q] + to)[lane];
+        for (int q = 0; q < F; ++q) {
+            const u32x4* from = (const u32x4*)(w[q] + to) + lane;
+            // past the caches where few an expert has more than one tile (8 x 8 rows, 11008 -> 4096: 22 against 24 us; with
+            // two tiles to an expert 43 against 40)
+            next[q] = MT == 1 ? __builtin_nontemporal_load(from) : *from;
+        }
     };
     fetch(wave);   // on its way while the rows are looked up
     const int8_t* row[MT];
@@ -81,7 +87,7 @@ __global__ __launch_bounds__(64 * waves_of(F), MT * F > 4 ? 3 : 4) void k_expert
     for (int c = wave; c < chunks; c += WAVES) {
         uint32_t bits[F][4];
 #pragma unroll
-        for (int q = 0; q < F; ++q) { bits[q][0] = next[q].x; bits[q][1] = next[q].y; bits[q][2] = next[q].z; bits[q][3] = next[q].w; }
+        for (int q = 0; q < F; ++q) { bits[q][0] = next[q][0]; bits[q][1] = next[q][1]; bits[q][2] = next[q][2]; bits[q][3] = next[q][3]; }
         fetch(c + WAVES);
         const auto step = [&](int s, const v4i (&x)[MT]) {
 #pragma unroll
