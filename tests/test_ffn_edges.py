@@ -1,0 +1,43 @@
+"""The binding's checks of feed-forward calls, without a GPU: tensors that would
+let a kernel past the caller's memory, or have it read other values."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+
+@pytest.fixture
+def on_host(monkeypatch):
+    """Host tensors pass for device tensors; launches are recorded in `calls` and left out."""
+    import xnor_popcount_gemm_amd as bnn
+    bnn.lib()
+
+    def dev(t, dtype, name):
+        assert t.dtype is dtype, name
+        return t
+
+    calls = []
+    monkeypatch.setattr(bnn, "_dev", dev)
+    monkeypatch.setattr(bnn, "_on", lambda index, call, *args: calls.append(args) or 0)
+    bnn.calls = calls
+    yield bnn
+    del bnn.calls
+
+
+def planes_out(M, Xb):
+    return {"Xb": Xb, "xsum": torch.zeros(M, dtype=torch.int32), "xscale": torch.zeros(M)}
+
+
+@pytest.mark.parametrize("M", [1, 2, 5])
+def test_planes_with_gaps_are_refused(on_host, M):
+    """A row of planes is written up to its stride: a view of part of wider rows would have its neighbours overwritten, and
+    the last one words past the end of its memory."""
+    x = torch.zeros(M, 1000)
+    big = torch.zeros(M, 8, 64, dtype=torch.int32)
+    for view in (big[:, :, :32], big[:, :, 32:], big[:, :, 4:36]):
+        with pytest.raises(ValueError, match="between its rows"):
+            on_host.block_norm(x, out=planes_out(M, view))
+    assert not on_host.calls
+    on_host.block_norm(x, out=planes_out(M, big))
+    on_host.block_norm(x, out=planes_out(M, torch.zeros(M, 8, 32, dtype=torch.int32)))
+    assert len(on_host.calls) == 2

@@ -1114,6 +1114,8 @@ def block_norm(x: torch.Tensor | None = None, branch: torch.Tensor | None = None
         if _dev(Xb, torch.int32, "out['Xb']").dim() != 3 or Xb.shape[0] != M or Xb.get_device() != index:
             raise ValueError(f"out['Xb'] must be [{M}, 8, ld] on cuda:{index}")
         bits = Xb.data_ptr() or _EMPTY, _planes_ld(Xb)
+        if Xb.shape[2] != bits[1]:   # all ld words of a plane are written
+            raise ValueError(f"out['Xb'] must have no words between its rows (got {Xb.shape[2]} words at a stride of {bits[1]})")
     if place is not None:
         if place.dim() != 2 or place.shape[0] != M or (weight is not None and weight.shape != place.shape):
             raise ValueError(f"place and weight must be [{M}, parts] alike")
