@@ -41,3 +41,24 @@ def test_planes_with_gaps_are_refused(on_host, M):
     on_host.block_norm(x, out=planes_out(M, big))
     on_host.block_norm(x, out=planes_out(M, torch.zeros(M, 8, 32, dtype=torch.int32)))
     assert len(on_host.calls) == 2
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on another device."""
+
+    def get_device(self):
+        return 1
+
+
+def test_route_workspace_on_another_device_is_refused(on_host):
+    """Its address goes to the kernel as it is."""
+    logits = torch.zeros(100, 8)
+    have = on_host.expert_route_workspace(100, 8, 2, device="cpu")
+    with pytest.raises(ValueError, match="workspace"):
+        on_host.expert_route(logits, 2, workspace=have.as_subclass(Elsewhere))
+    with pytest.raises(ValueError, match="workspace"):
+        on_host.expert_route(logits, 2, workspace=torch.zeros(2 * have.numel(), dtype=torch.uint8)[::2])
+    assert not on_host.calls
+    on_host.expert_route(logits, 2, workspace=have)
+    on_host.expert_route(logits, 2)
+    assert len(on_host.calls) == 2

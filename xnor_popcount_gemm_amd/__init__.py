@@ -1031,6 +1031,13 @@ def _vector(t: torch.Tensor | None, dtype, name: str, n: int, index: int) -> int
     return t.data_ptr() or _EMPTY
 
 
+def _workspace(t: torch.Tensor, index: int):
+    """Address and bytes of a workspace on device `index`."""
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{index} (got strides {t.stride()} on {t.device})")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
@@ -1158,8 +1165,10 @@ def expert_route(logits: torch.Tensor, top: int, *, score: str = "softmax", bias
     offsets[e + 1] - 1), ``order`` int32 [rows * top] (row * top + choice of
     each position), ``place`` int32 [rows, top] (its inverse; -1: none).
     ``out``: such a dict of tensors to write instead.  ``workspace``:
-    expert_route_workspace, made here where it is None."""
+    expert_route_workspace on the device of ``logits``, made here where it is
+    None."""
     rows, experts = logits.shape
+    index = _dev(logits, logits.dtype, "logits").get_device()
     L = _lib or lib()
     if out is None:
         pair = dict(dtype=torch.int32, device=logits.device)
@@ -1167,13 +1176,13 @@ def expert_route(logits: torch.Tensor, top: int, *, score: str = "softmax", bias
                "offsets": torch.empty(experts + 1, **pair), "order": torch.empty(rows * top, **pair), "place": torch.empty((rows, top), **pair)}
     if workspace is None:
         workspace = torch.empty(max(0, L.bnn_expert_route_workspace(rows, experts, top)), dtype=torch.uint8, device=logits.device)
-    n, index, i32 = rows * top, _dev(logits, logits.dtype, "logits").get_device(), torch.int32
+    n, i32 = rows * top, torch.int32
     a = _pack_route(*_matrix(logits, logits.dtype, "logits", rows, experts, index), _float_type(logits, "logits"), rows, experts, top,
                     _vector(used, i32, "used", 1, index), _one_of(SCORES, score, "score"), _vector(bias, torch.float32, "bias", experts, index),
                     1 if renorm else 0, scale, _vector(out["expert"], i32, "out['expert']", n, index),
                     _vector(out["weight"], torch.float32, "out['weight']", n, index), _vector(out["offsets"], i32, "out['offsets']", experts + 1, index),
                     _vector(out["order"], i32, "out['order']", n, index), _vector(out["place"], i32, "out['place']", n, index),
-                    workspace.data_ptr(), workspace.numel() * workspace.element_size())
+                    *_workspace(workspace, index))
     _check(_on(index, L.bnn_expert_route, a), "bnn_expert_route")
     return out
 
