@@ -62,3 +62,22 @@ def test_route_workspace_on_another_device_is_refused(on_host):
     on_host.expert_route(logits, 2, workspace=have)
     on_host.expert_route(logits, 2)
     assert len(on_host.calls) == 2
+
+
+@pytest.mark.parametrize("ternary", [False, True])
+@pytest.mark.parametrize("E", [1, 3])
+def test_planes_narrower_than_k_are_refused(on_host, E, ternary):
+    """A view of a few words of wider rows has the stride of K but not its words."""
+    wide = torch.zeros(E, 5, 16, dtype=torch.int32)
+    alpha = torch.ones(E, 5)
+
+    def lay_out(w, K):
+        on_host.ExpertWeights(w, K, Zp=w if ternary else None, alpha=alpha)
+    for view in (wide[:, :, :3], wide[:, :, 12:15], wide[:, :, 16:]):
+        with pytest.raises(ValueError, match="words of K = 100"):
+            lay_out(view, 100)
+    assert not on_host.calls
+    lay_out(wide[:, :, 12:], 100)
+    lay_out(wide[:, :, :3], 96)
+    lay_out(wide, 512)
+    assert len(on_host.calls) == 3

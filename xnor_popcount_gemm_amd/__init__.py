@@ -1211,6 +1211,8 @@ class ExpertWeights:
         n = lib().bnn_expert_pack_bytes(self.experts, self.N, self.K, self.ternary)
         if n < 0:
             raise ValueError("ExpertWeights: sizes out of range")
+        if Wp.shape[2] < (self.K + 31) // 32:   # a stride of so many words is not enough: a narrow view ends before
+            raise ValueError(f"Wp must have the {(self.K + 31) // 32} words of K = {self.K} (got {Wp.shape[2]})")
         self.W = torch.empty(n, dtype=torch.uint8, device=Wp.device)
         index = self._index = Wp.get_device()
         _check(_on(index, lib().bnn_expert_pack, Wp.data_ptr() or _EMPTY, 0 if Zp is None else Zp.data_ptr() or _EMPTY, Wp.stride(1), Wp.stride(0),
