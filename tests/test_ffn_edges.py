@@ -81,3 +81,11 @@ def test_planes_narrower_than_k_are_refused(on_host, E, ternary):
     lay_out(wide[:, :, :3], 96)
     lay_out(wide, 512)
     assert len(on_host.calls) == 3
+
+
+def test_nonzero_plane_on_another_device_is_refused(on_host):
+    S = torch.zeros(2, 5, 4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="device"):
+        on_host.ExpertWeights(S, 100, Zp=torch.zeros_like(S).as_subclass(Elsewhere), alpha=torch.ones(2))
+    assert not on_host.calls
+    on_host.ExpertWeights(S, 100, Zp=torch.zeros_like(S), alpha=torch.ones(2))

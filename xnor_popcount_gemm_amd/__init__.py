@@ -1204,8 +1204,8 @@ class ExpertWeights:
             Zp = Zp[None] if Zp is not None and Zp.dim() == 2 else Zp
         if Wp.dim() != 3 or Wp.stride(2) != 1:
             raise ValueError("Wp must be [N, ld] or [experts, N, ld] with a unit last stride")
-        if Zp is not None and (_dev(Zp, torch.int32, "Zp").shape != Wp.shape or Zp.stride() != Wp.stride()):
-            raise ValueError("Zp must be laid out as Wp")
+        if Zp is not None and (_dev(Zp, torch.int32, "Zp").shape != Wp.shape or Zp.stride() != Wp.stride() or Zp.get_device() != Wp.get_device()):
+            raise ValueError("Zp must be laid out as Wp, on its device")
         self.experts, self.N, self.K, self.ternary = Wp.shape[0], Wp.shape[1], int(K), Zp is not None
         self.device = Wp.device
         n = lib().bnn_expert_pack_bytes(self.experts, self.N, self.K, self.ternary)
