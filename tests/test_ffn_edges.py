@@ -89,3 +89,18 @@ def test_nonzero_plane_on_another_device_is_refused(on_host):
         on_host.ExpertWeights(S, 100, Zp=torch.zeros_like(S).as_subclass(Elsewhere), alpha=torch.ones(2))
     assert not on_host.calls
     on_host.ExpertWeights(S, 100, Zp=torch.zeros_like(S), alpha=torch.ones(2))
+
+
+@pytest.mark.parametrize("E,N", [(2, 5), (7, 5), (4, 1), (3, 3)])
+def test_scales_that_experts_share(on_host, E, N):
+    """A row stride of 0 means one scale for each expert to the kernel, so the row is laid out for each of them."""
+    S = torch.zeros(E, N, 4, dtype=torch.int32)
+    row = torch.arange(1.0, N + 1)
+    for alpha in (row.expand(E, N), row[:1].expand(E, N), row[:1, None].expand(E, N)):
+        w = on_host.ExpertWeights(S, 100, alpha=alpha)
+        address, stride = w._c[1:3]
+        assert stride >= N and address == w.alpha.data_ptr() and w.alpha.is_contiguous() and torch.equal(w.alpha, alpha)
+    own = torch.rand(E, N + 3)[:, :N]
+    w = on_host.ExpertWeights(S, 100, alpha=own)      # rows with gaps are read where they are
+    assert w._c[1:3] == (own.data_ptr(), N + 3)
+    assert on_host.ExpertWeights(S, 100, alpha=torch.ones(E))._c[2] == 0

@@ -1193,9 +1193,10 @@ class ExpertWeights:
 
     ``Wp``, ``Zp``: the planes of pack_weights (``Zp`` None) or
     pack_weights_ternary, [N, ld] of a single layer or [experts, N, ld]
-    stacked.  ``alpha`` float32 [experts, N] ([N] of a single layer), or
-    [experts] with one scale for a whole matrix; ``bias`` float32 like
-    [experts, N], or None.  The planes are not needed afterwards."""
+    stacked.  ``alpha`` float32 [experts, N] ([N] of a single layer; a row
+    that experts share, as by ``expand``, is copied for each), or [experts]
+    with one scale for a whole matrix; ``bias`` float32 like [experts, N], or
+    None.  The planes are not needed afterwards."""
 
     def __init__(self, Wp: torch.Tensor, K: int, *, Zp: torch.Tensor | None = None, alpha: torch.Tensor, bias: torch.Tensor | None = None):
         _dev(Wp, torch.int32, "Wp")
@@ -1223,6 +1224,8 @@ class ExpertWeights:
         if alpha.shape == (self.experts,):
             scale = _vector(alpha, torch.float32, "alpha", self.experts, index), 0
         else:
+            if alpha.dim() == 2 and self.experts > 1 and alpha.stride(0) < self.N:
+                alpha = alpha.contiguous()   # a row that experts share: a stride of 0 would say that each has a single scale
             scale = _matrix(alpha, torch.float32, "alpha", self.experts, self.N, index)
         shift = 0, 0
         if bias is not None:
