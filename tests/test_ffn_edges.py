@@ -104,3 +104,13 @@ def test_scales_that_experts_share(on_host, E, N):
     w = on_host.ExpertWeights(S, 100, alpha=own)      # rows with gaps are read where they are
     assert w._c[1:3] == (own.data_ptr(), N + 3)
     assert on_host.ExpertWeights(S, 100, alpha=torch.ones(E))._c[2] == 0
+
+
+@pytest.mark.parametrize("name", ["W", "alpha", "bias"])
+def test_weights_tensors_cannot_be_replaced(on_host, name):
+    """The calls read them by the addresses that they had: another tensor in their place would leave those to be freed."""
+    w = on_host.ExpertWeights(torch.zeros(2, 5, 4, dtype=torch.int32), 100, alpha=torch.ones(2, 5), bias=torch.zeros(2, 5))
+    held = getattr(w, name)
+    with pytest.raises(AttributeError):
+        setattr(w, name, 2 * held)
+    assert getattr(w, name) is held and held.data_ptr() in w._c

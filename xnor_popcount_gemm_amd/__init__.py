@@ -1196,7 +1196,8 @@ class ExpertWeights:
     stacked.  ``alpha`` float32 [experts, N] ([N] of a single layer; a row
     that experts share, as by ``expand``, is copied for each), or [experts]
     with one scale for a whole matrix; ``bias`` float32 like [experts, N], or
-    None.  The planes are not needed afterwards."""
+    None.  The planes are not needed afterwards; ``alpha`` and ``bias`` are
+    kept and read by each call."""
 
     def __init__(self, Wp: torch.Tensor, K: int, *, Zp: torch.Tensor | None = None, alpha: torch.Tensor, bias: torch.Tensor | None = None):
         _dev(Wp, torch.int32, "Wp")
@@ -1214,10 +1215,10 @@ class ExpertWeights:
             raise ValueError("ExpertWeights: sizes out of range")
         if Wp.shape[2] < (self.K + 31) // 32:   # a stride of so many words is not enough: a narrow view ends before
             raise ValueError(f"Wp must have the {(self.K + 31) // 32} words of K = {self.K} (got {Wp.shape[2]})")
-        self.W = torch.empty(n, dtype=torch.uint8, device=Wp.device)
+        W = torch.empty(n, dtype=torch.uint8, device=Wp.device)
         index = self._index = Wp.get_device()
         _check(_on(index, lib().bnn_expert_pack, Wp.data_ptr() or _EMPTY, 0 if Zp is None else Zp.data_ptr() or _EMPTY, Wp.stride(1), Wp.stride(0),
-                   self.experts, self.N, self.K, self.W.data_ptr() or _EMPTY, n), "bnn_expert_pack")
+                   self.experts, self.N, self.K, W.data_ptr() or _EMPTY, n), "bnn_expert_pack")
         _dev(alpha, torch.float32, "alpha")
         if alpha.shape == (self.N,) and self.experts == 1 and self.N != 1:
             alpha = alpha[None]
@@ -1230,8 +1231,13 @@ class ExpertWeights:
         shift = 0, 0
         if bias is not None:
             shift = _matrix(bias[None] if bias.dim() == 1 else bias, torch.float32, "bias", self.experts, self.N, index)
-        self.alpha, self.bias = alpha, bias
-        self._c = (self.W.data_ptr() or _EMPTY, *scale, *shift)
+        self._held = W, alpha, bias
+        self._c = (W.data_ptr() or _EMPTY, *scale, *shift)
+
+    # Their addresses are in _c: they can be written in place, not replaced.
+    W = property(lambda self: self._held[0])
+    alpha = property(lambda self: self._held[1])
+    bias = property(lambda self: self._held[2])
 
 
 def expert_linear(Xq: torch.Tensor, weights: ExpertWeights, *, xscale: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
