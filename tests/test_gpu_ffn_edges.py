@@ -38,3 +38,45 @@ def test_activations_at_the_ends(bnn, P, act):
     banner(f"ends {P} {act}")
     y = bnn.expert_linear(torch.zeros((P, 16), dtype=torch.int8, device="cuda"), W, act=act)[P - 1].cpu()
     assert torch.equal(y[:4], z[:4].cpu()) and (y[4:10] == 0).all() and torch.isnan(y[10:]).all()
+
+
+def tiles_of_128(E, P, N, gated):
+    """Whether the products take tiles of 128 positions: 96 rows to an expert, and two workgroups to each compute unit."""
+    cols = 128 if gated else 256
+    return P // E >= 96 and (P + min(E, P) * 127) // 128 * -(-N // cols) >= 512
+
+
+@pytest.mark.parametrize("E,P,N,K", [(4, 3000, 6200, 768), (4, 3000, 6200, 896), (4, 3000, 6200, 1024), (4, 3000, 6200, 1152), (4, 3000, 6200, 1300), (2, 3000, 6200, 1408),
+                                     (2, 3000, 6200, 2100), (2, 3000, 6200, 4096)])
+@pytest.mark.parametrize("ternary", [True, False])
+@pytest.mark.parametrize("gated", [False, True])
+def test_linear_long_rows_of_wide_grids(bnn, E, P, N, K, ternary, gated):
+    """Tiles of 128 positions over many stages, one turn of the ring and several, whole and with a rest: every output.
+    The sums are whole numbers, and products, comparisons and the last rounding are the same in torch, bit for bit."""
+    rng = np.random.default_rng(K)
+    if gated:
+        N //= 2
+    assert tiles_of_128(E, P, N, gated)
+    banner(f"wide grid E={E} P={P} N={N} K={K} ternary={ternary} gated={gated}")
+    mats = [matrices(bnn, rng, E, N, K, ternary, h == 0, h == 1) for h in range(2 if gated else 1)]
+    R, top = (700, 5) if gated else (P, 1)
+    order = torch.from_numpy(rng.integers(0, R * top, P).astype(np.int32)).cuda() if gated else None
+    offsets = split(rng, P, E, "ragged")
+    Xq = int8_rows(bnn, rng, R, K)
+    xs = torch.from_numpy((0.01 + 0.02 * rng.random(R)).astype(np.float32)).cuda()
+    kind = torch.bfloat16 if gated else torch.float32
+    got = bnn.expert_linear(Xq, mats[0][3], xscale=xs, offsets=torch.from_numpy(offsets).cuda(), order=order, per_row=top, up=mats[1][3] if gated else None,
+                            act="relu2" if gated else "none", out_dtype=kind)
+    torch.cuda.synchronize()
+    row = (order // top).long() if gated else torch.arange(P, device="cuda")
+    for e in range(E):
+        at = row[offsets[e]:offsets[e + 1]]
+        x, z = Xq[at].double(), []
+        for t, alpha, bias, _ in mats:
+            D = torch.matmul(x, torch.from_numpy(t[e]).cuda().double().t().contiguous()).float()
+            v = alpha[e] * D * xs[at][:, None]
+            z.append(v if bias is None else v + bias[e])
+        want = z[0]
+        if gated:
+            want = torch.where(want < 0, torch.zeros_like(want), want * want) * z[1]
+        assert torch.equal(got[offsets[e]:offsets[e + 1]], want.to(kind)), f"expert {e}"
