@@ -80,3 +80,21 @@ def test_linear_long_rows_of_wide_grids(bnn, E, P, N, K, ternary, gated):
         if gated:
             want = torch.where(want < 0, torch.zeros_like(want), want * want) * z[1]
         assert torch.equal(got[offsets[e]:offsets[e + 1]], want.to(kind)), f"expert {e}"
+
+
+@pytest.mark.parametrize("E", [2, 5])
+@pytest.mark.parametrize("P", [6, 300])
+def test_linear_shared_scales(bnn, E, P):
+    """One row of scales for all experts, expanded; more experts than columns too."""
+    rng = np.random.default_rng(29)
+    for N in (40, 3):
+        t, _, _, W = matrices(bnn, rng, E, N, 96, True, False, False)
+        row = 0.02 * (1 + 0.3 * make(rng, N))
+        planes = [bnn.pack_weights_ternary(m, delta=0.5) for m in torch.from_numpy(t.astype(np.float32)).cuda()]
+        W = bnn.ExpertWeights(torch.stack([p[0] for p in planes]), 96, Zp=torch.stack([p[1] for p in planes]), alpha=row.expand(E, N))
+        Xq, offsets = int8_rows(bnn, rng, P, 96), split(rng, P, E, "ragged")
+        banner(f"shared scales E={E} P={P} N={N}")
+        y = bnn.expert_linear(Xq, W, offsets=torch.from_numpy(offsets).cuda())
+        torch.cuda.synchronize()
+        want, off, _ = ref.expert_linear(Xq, t, row.expand(E, N).contiguous(), offsets=offsets)
+        near(y, want, off, torch.float32, f"shared scales {N}")
