@@ -98,3 +98,23 @@ def test_linear_shared_scales(bnn, E, P):
         torch.cuda.synchronize()
         want, off, _ = ref.expert_linear(Xq, t, row.expand(E, N).contiguous(), offsets=offsets)
         near(y, want, off, torch.float32, f"shared scales {N}")
+
+
+def test_route_workspace_used_again(bnn):
+    """One workspace, larger than most calls need, with what the last call left in it."""
+    rng = np.random.default_rng(30)
+    work = bnn.expert_route_workspace(5000, 200, 8)
+    work.fill_(255)
+    for rows, E, top in ((5000, 200, 8), (40, 7, 2), (33, 200, 5), (5000, 3, 1), (1, 200, 8), (700, 64, 6), (4100, 130, 8)):
+        l = make(rng, (rows, E))
+        banner(f"workspace again {rows} {E}")
+        got = bnn.expert_route(l, top, workspace=work)
+        torch.cuda.synchronize()
+        expert, weight, offsets, order, place = ref.expert_route(l, top)
+        for name, want in (("expert", expert), ("offsets", offsets), ("order", order), ("place", place)):
+            np.testing.assert_array_equal(got[name].cpu().numpy(), want, err_msg=f"{name} {rows} {E}")
+    for bad in (work.cpu(), work[::2], torch.empty(0, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="workspace"):
+            bnn.expert_route(make(rng, (100, 8)), 2, workspace=bad)
+    with pytest.raises(bnn.BnnError):
+        bnn.expert_route(make(rng, (100, 8)), 2, workspace=work[:16])
