@@ -118,3 +118,19 @@ def test_route_workspace_used_again(bnn):
             bnn.expert_route(make(rng, (100, 8)), 2, workspace=bad)
     with pytest.raises(bnn.BnnError):
         bnn.expert_route(make(rng, (100, 8)), 2, workspace=work[:16])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("pre", ["none", "rms", "layer"])
+@pytest.mark.parametrize("D", [96, 1001, 4096])
+def test_norm_scale_is_of_the_rows_before_they_are_rounded(bnn, kind, pre, D):
+    """xscale with a 16-bit y: max |v| of the 64-bit rows / 127, fp32 roundings of v and of the quotient."""
+    rng = np.random.default_rng(31)
+    x, b = make(rng, (6, D), by=3.0), make(rng, (6, D), KINDS[kind])
+    banner(f"xscale {kind} {pre} {D}")
+    got = bnn.block_norm(x, b, pre=pre, y_dtype=KINDS[kind])
+    torch.cuda.synchronize()
+    _, stored, v = ref.block_norm(x, b, pre=pre)
+    most = np.abs(v).max(-1)
+    assert (np.abs(ref.f64(got["xscale"]) - most / 127) <= 2.01 * ref.E32 * most / 127).all()
+    near(got["y"], v, ref.E32 * np.abs(v) + 2.0 ** -40 * most[:, None], KINDS[kind], "y")
