@@ -134,3 +134,21 @@ def test_norm_scale_is_of_the_rows_before_they_are_rounded(bnn, kind, pre, D):
     most = np.abs(v).max(-1)
     assert (np.abs(ref.f64(got["xscale"]) - most / 127) <= 2.01 * ref.E32 * most / 127).all()
     near(got["y"], v, ref.E32 * np.abs(v) + 2.0 ** -40 * most[:, None], KINDS[kind], "y")
+
+
+@pytest.mark.parametrize("rows,used", [(1, 1), (9, 9), (40, 33), (600, 590)])
+def test_feed_forward_into_the_next_block(bnn, rows, used):
+    """The join at the end of a step: its norm and its INT8 rows, from what the products gave."""
+    rng = np.random.default_rng(18)
+    m = Experts(bnn, rng)
+    x, att = make(rng, (rows, 192), torch.bfloat16, 2.0), make(rng, (rows, 192))
+    banner(f"next block {rows}")
+    n, r, h, d, z = m(x, att, torch.tensor([used], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    s, _, _ = ref.block_norm(n["x"][:used], d[:used * m.top], place=r["place"][:used], weight=r["weight"][:used], pre_weight=m.w3)
+    near(z["x"][:used], s, ref.E32 * np.abs(s), torch.bfloat16, "x")
+    v = ref.norm(ref.f64(z["x"][:used]), "rms", m.w3, None, 1e-6)      # the norm reads the stream as it is stored
+    near(z["y"][:used], v, ref.E32 * np.abs(v) + 2.0 ** -40 * np.abs(v).max(-1, keepdims=True), torch.float32, "y")
+    code, scale, _ = ref.quantized(z["y"][:used].cpu().numpy())
+    np.testing.assert_array_equal(z["Xq"][:used].cpu().numpy(), code)
+    np.testing.assert_array_equal(z["xscale"][:used].cpu().numpy(), scale)
