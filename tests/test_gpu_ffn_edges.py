@@ -152,3 +152,29 @@ def test_feed_forward_into_the_next_block(bnn, rows, used):
     code, scale, _ = ref.quantized(z["y"][:used].cpu().numpy())
     np.testing.assert_array_equal(z["Xq"][:used].cpu().numpy(), code)
     np.testing.assert_array_equal(z["xscale"][:used].cpu().numpy(), scale)
+
+
+@pytest.mark.parametrize("rows", [20, 300])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_small_scores(bnn, rows, renorm):
+    """Sigmoids of logits from -87 to -103: numbers below the normal ones, not zeros.  Roundings, in half steps of fp32:
+    exponential 2, sum 1, quotient 1, and a step or two of the smallest number, d; the renormalized ones from scores w, w_i off by
+    that much each: a quotient of w + d and their sum."""
+    rng = np.random.default_rng(32)
+    l = torch.from_numpy(rng.uniform(-103, -87, (rows, 40)).astype(np.float32)).cuda()
+    l[3] = -200.0                                                # nothing left: weights 0
+    banner(f"small scores {rows} {renorm}")
+    got = bnn.expert_route(l, 4, score="sigmoid", renorm=renorm)
+    torch.cuda.synchronize()
+    w = np.exp(-np.sort(-ref.f64(l), 1)[:, :4])
+    d = 4 * ref.E32 * w + 2 * 2.0 ** -149
+    have = ref.f64(got["weight"])
+    if renorm:
+        live = w.sum(1) > 2.0 ** -140
+        assert live.sum() > rows / 2
+        total = w.sum(1, keepdims=True)
+        assert (np.abs(have - w / total) <= (d + w / total * d.sum(1, keepdims=True)) / (total - d.sum(1, keepdims=True)) + 6 * ref.E32)[live].all()
+        assert (np.abs(have[live].sum(1) - 1) <= 16 * ref.E32).all()
+    else:
+        assert (np.abs(have - w) <= d).all()
+    assert (have[3] == 0).all()

@@ -139,7 +139,9 @@ __device__ void choose(const RouteArgs& a, int row, int lane, uint32_t* count) {
     float w = 0.f;
     if (mine >= 0) {
         const float lg = logit_at(lr, mine, a.type);
-        w = a.sigmoid ? 1.f / (1.f + expf(-lg)) : expf(lg - most) / total;
+        const float ex = expf(a.sigmoid ? -fabsf(lg) : lg - most);
+        // a sigmoid by exp(-|l|): exp(-l) overflows at -88.7, where the score is still a number
+        w = a.sigmoid ? (lg < 0.f ? ex : 1.f) / (1.f + ex) : ex / total;
         atomicAdd(&count[mine], 1u);
     }
     if (a.renorm) {
