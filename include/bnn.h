@@ -693,8 +693,10 @@ typedef struct bnn_norm_args {
  *     x_out[m] = s;    y = pre(s);    Y[m] = y
  *     Xq[m], Xb[m], xsum[m], xscale[m] = INT8 rows of y as bnn_quantize_act_i8
  *                                        lays them out, with inv = fl32(127
- *                                        fl32(1 / amax)): a code next to a
- *                                        border may be the neighbouring one
+ *                                        fl32(1 / amax)), one rounding more
+ *                                        than there: of 10^7 codes two or three,
+ *                                        next to a border, are the neighbouring
+ *                                        ones
  * Everything up to y is computed in 64 bits, s is rounded to x's type where
  * x_out is given (pre then reads the rounded stream, as a call of its own on
  * x_out would) and y to fp32; 16-bit outputs are rounded from fp32.  The

@@ -6,12 +6,18 @@
 //     q = rint(fl32(y) * fl32(127 * fl32(1 / max|y|)))
 //
 // Bound by memory traffic: each value is read once, held in registers through
-// its three or four row sums, and written once.  All arithmetic up to fl32(y)
+// its reductions, and written once: an RMS norm with codes has two (squares,
+// largest value), layer norms on both sides with planes six (two a norm, largest
+// value, sum of the codes).  All arithmetic up to fl32(y)
 // is in 64 bits, so codes and scales do not depend on the order of a sum; that
 // costs about 10 of the 25 operations of a value.  8192 rows of 4096, fp32
 // stream + two experts' rows -> stream, output, codes: 124 us, 5.15 TB/s, what a plain
 // copy reaches; 16384 rows of 11008 bfloat16 -> codes, 3 bytes a value: 153 us,
-// 3.5 TB/s, where the operations bound it; one row: 6.7 us, its three sums.
+// 3.5 TB/s, where the operations bound it; one row: 6.7 us, its three reductions.
+// Not near a copy: rows held in 64 bits past 8192 values, which spill 58
+// registers (16384 x 11008 with a norm of the branch: 701 us, 1.8 TB/s), and
+// operands that are not 4-aligned, value by value (8192 x 4097: 151 us, 48 for
+// 4096).
 //
 // A row belongs to T threads (a wave, or up to 16 waves of a workgroup),
 // thread t holds the 4-value groups t, t + T, ... of it.  Rows are read and

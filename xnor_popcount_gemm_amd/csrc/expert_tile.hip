@@ -22,10 +22,10 @@
 // tiles, in groups of 8 position tiles by weight tile, so that what is in its
 // L2 is used again.
 //
-// 8192^3 ternary: 391 us, 2811 TOPS (a library's int8 product 2082).  16384
-// positions of 8 experts, 4096 -> 2 x 11008 with a gate: 1232-1262 us, 2340-2400 TOPS:
-// matrix instructions take 57% of the cycles and vector instructions, which a
-// SIMD does not issue beside them, 34%.
+// 8192^3 ternary: 404-411 us, 2680-2720 TOPS (the library's int8 product of the
+// same values 415-423).  16384 positions of 8 experts, 4096 -> 2 x 11008 with a
+// gate: 1239-1247 us, 2370-2390 TOPS: matrix instructions take 57% of the cycles
+// and vector instructions, which a SIMD does not issue beside them, 39%.
 #include <type_traits>
 
 #include "expert_kernel.hpp"

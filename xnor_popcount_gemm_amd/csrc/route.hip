@@ -25,7 +25,7 @@ namespace {
 
 constexpr int MAX_EXPERTS = 1024;
 constexpr int THREADS = 1024, WAVES = THREADS / 64;
-constexpr int MAX_PARTS = 256;       // workgroups that share the rows, 16 or more to each
+constexpr int MAX_PARTS = 256;       // workgroups that share the rows; with fewer a workgroup has at most 16
 constexpr int ONE_PART_ROWS = 32;    // rows that one workgroup takes in one launch
 
 // Keys in the order of an unsigned integer, in two words; 0 for what is never
