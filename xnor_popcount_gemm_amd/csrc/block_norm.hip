@@ -29,8 +29,6 @@
 namespace bnn {
 namespace {
 
-typedef double f64x4 __attribute__((ext_vector_type(4)));
-
 // A row of `count` values of a type: loads past its end give zeros and stores
 // there are dropped, without a branch (VEC: 4 values at a time, count a
 // multiple of 4; otherwise one by one).
@@ -83,8 +81,6 @@ struct Row {
 #pragma unroll
             for (int i = 0; i < 4; ++i) __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(v >> (8 * i)), r, e0 + i, 0, 0);
     }
-
-    __device__ __forceinline__ f32x4 floats(int e0) const { return __builtin_bit_cast(f32x4, load(e0, T_F32)); }
 };
 
 __device__ __forceinline__ f32x4 values(u32x4 v, int type) {
