@@ -8,7 +8,7 @@ import torch
 
 import ffn_ref as ref
 from gpu_util import banner
-from test_gpu_ffn import KINDS, Experts, bnn, int8_rows, make, matrices, near, split  # noqa: F401 (bnn: the fixture)
+from test_gpu_ffn import KINDS, LEFT, Experts, bnn, int8_rows, make, matrices, near, split  # noqa: F401 (bnn: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -178,3 +178,38 @@ def test_route_small_scores(bnn, rows, renorm):
     else:
         assert (np.abs(have - w) <= d).all()
     assert (have[3] == 0).all()
+
+
+@pytest.mark.parametrize("M,D", [((1 << 23) + 3, 2), ((1 << 20) + 5, 516)])
+def test_norm_more_workgroups_than_one_dimension(bnn, M, D):
+    """Past 2^20 workgroups a launch has two dimensions: four rows to each, and one."""
+    banner(f"norm {M} x {D}")
+    x = (torch.arange(M * D, device="cuda", dtype=torch.int32) % 251 - 125).reshape(M, D).to(torch.bfloat16)
+    used = torch.tensor([M - 2], dtype=torch.int32).cuda()
+    out = {"y": torch.full((M, D), LEFT, dtype=torch.bfloat16, device="cuda")}
+    bnn.block_norm(x, x_scale=0.5, pre="none", used=used, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out["y"][:M - 2], x[:M - 2] * 0.5) and (out["y"][M - 2:] == LEFT).all()
+
+
+def test_linear_more_workgroups_than_one_dimension(bnn):
+    """2^24 outputs of few rows: 2^21 workgroups.  K = 1, so that y is a product of numbers."""
+    N, P = 1 << 24, 80
+    banner("linear 2^21 workgroups")
+    gen = torch.Generator(device="cuda").manual_seed(33)
+    q = torch.zeros((P, 16), dtype=torch.int8, device="cuda")
+    q[:, 0] = torch.arange(P, device="cuda") - 40
+    offsets = torch.tensor([0, 47, P], dtype=torch.int32, device="cuda")
+    weights, signs = [], []
+    for _ in range(2):
+        S, Z = (torch.randint(0, 2, (2, N, 4), dtype=torch.int32, device="cuda", generator=gen) for _ in range(2))
+        alpha = torch.tensor([0.5, 2.0], device="cuda")
+        weights.append(bnn.ExpertWeights(S, 1, Zp=Z, alpha=alpha))
+        signs.append((Z[:, :, 0] * (1 - 2 * S[:, :, 0])).to(torch.int8))
+        del S, Z
+    y = bnn.expert_linear(q[:, :1], weights[0], offsets=offsets, up=weights[1], out_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    for p in range(P):
+        e = int(p >= 47)
+        d = (signs[0][e] * signs[1][e]).to(torch.bfloat16) * float((p - 40) ** 2 * (0.25, 4.0)[e])     # a product of fp32 numbers, rounded once
+        assert torch.equal(y[p], d), p
