@@ -176,6 +176,23 @@ def test_attention_with_a_workspace_of_other_sizes(bnn, heads, kv, dim, seqs, no
             assert torch.allclose(out[:rows], results[0][0][:rows], rtol=0, atol=8e-4) and torch.allclose(lse[:rows], results[0][1][:rows], rtol=0, atol=4e-4)
 
 
+def test_workspaces_elsewhere_are_refused(bnn):
+    """One in host memory, and one with gaps: their addresses would go to the kernels as they are."""
+    banner("workspaces elsewhere")
+    normal = lambda *shape: torch.zeros(shape, device="cuda")
+    k = normal(4, 64, 2, 64).to(BF)
+    cache = bnn.KVCache(k, k.clone(), cuda_i32([[0, 1, 2, 3]]), pos=cuda_i32(range(512)).reshape(1, 2, 256), score=normal(1, 2, 256))
+    indptr, ctx, q = cuda_i32([0, 1]), cuda_i32([200]), normal(1, 4, 64).to(BF)
+    attend = lambda w: bnn.tree_attention(q, cache, indptr, ctx, max_nodes=1, max_ctx=200, workspace=w)
+    evict = lambda w: bnn.cache_evict(cache, indptr, ctx, budget=40, recent=8, max_nodes=1, max_ctx=200, workspace=w)
+    for call, work in ((attend, bnn.tree_attention_workspace(cache, 1, 4, 1, 200)), (evict, bnn.cache_evict_workspace(cache))):
+        for bad in (work.cpu(), torch.empty(2 * work.numel(), dtype=torch.uint8, device="cuda")[::2]):
+            with pytest.raises(ValueError, match="workspace"):
+                call(bad)
+        call(work)
+    torch.cuda.synchronize()
+
+
 # ---- nothing to do
 
 def no_tokens(B, kv=2, heads=4, dim=64, n=40):

@@ -709,6 +709,13 @@ _KV_TYPES = {torch.bfloat16: BF16, torch.float16: F16}
 ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
 
 
+def _workspace(t: torch.Tensor, index: int):
+    """Address and bytes of a workspace on device `index`."""
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{index} (got strides {t.stride()} on {t.device})")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 class KVCache:
     """A paged key/value cache over the caller's tensors (bnn_kv_cache).
 
@@ -911,8 +918,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, indptr: torch.Tensor, ctx: t
         workspace = torch.empty(max(0, L.bnn_tree_attention_workspace(cache._ref, b, heads)), dtype=torch.uint8, device=q.device)
     a = _pack_attn(*_token_rows(q, cache.dtype, "q", rows, heads, cache.dim), heads, *_bit_rows(mask, "mask", rows),
                    dim ** -0.5 if scale is None else scale, *_token_rows(out, kind, "out", rows, heads, dim),
-                   F32 if kind is torch.float32 else _KV_TYPES[kind], *_row_floats(lse, "lse", rows, heads),
-                   workspace.data_ptr(), workspace.numel() * workspace.element_size())
+                   F32 if kind is torch.float32 else _KV_TYPES[kind], *_row_floats(lse, "lse", rows, heads), *_workspace(workspace, cache._index))
     _check(L.bnn_tree_attention(cache._ref, b, a, _raw_stream(cache._index)), "bnn_tree_attention")
     return out, lse
 
@@ -972,8 +978,8 @@ def cache_evict(cache: KVCache, indptr: torch.Tensor, ctx: torch.Tensor, *, budg
     if workspace is None:
         workspace = cache_evict_workspace(cache)
     a = _pack_evict(*_bit_rows(accept, "accept", ctx.numel()), budget, recent, cache.pos.data_ptr() or _EMPTY, pos_out.data_ptr() or _EMPTY,
-                    cache.score.data_ptr() or _EMPTY, score_out.data_ptr() or _EMPTY, slots[2], ctx_out.data_ptr() or _EMPTY, workspace.data_ptr(),
-                    workspace.numel() * workspace.element_size())
+                    cache.score.data_ptr() or _EMPTY, score_out.data_ptr() or _EMPTY, slots[2], ctx_out.data_ptr() or _EMPTY,
+                    *_workspace(workspace, cache._index))
     _check((_lib or lib()).bnn_cache_evict(cache._ref, _batch(cache, indptr, ctx, 1 << 30, max_nodes, max_ctx), a, _raw_stream(cache._index)),
            "bnn_cache_evict")
     return ctx_out
@@ -1030,13 +1036,6 @@ def _vector(t: torch.Tensor | None, dtype, name: str, n: int, index: int) -> int
         _dev(t, dtype, name)
         raise ValueError(f"{name} must be contiguous on cuda:{index}, with {n} elements (got {tuple(t.shape)} on {t.device})")
     return t.data_ptr() or _EMPTY
-
-
-def _workspace(t: torch.Tensor, index: int):
-    """Address and bytes of a workspace on device `index`."""
-    if t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on cuda:{index} (got strides {t.stride()} on {t.device})")
-    return t.data_ptr(), t.numel() * t.element_size()
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
