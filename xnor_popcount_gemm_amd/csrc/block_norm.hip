@@ -14,7 +14,7 @@
 // stream + two experts' rows -> stream, output, codes: 124 us, 5.15 TB/s, what a plain
 // copy reaches; 16384 rows of 11008 bfloat16 -> codes, 3 bytes a value: 153 us,
 // 3.5 TB/s, where the operations bound it; one row: 6.7 us, its three reductions.
-// Not near a copy: rows held in 64 bits past 8192 values, which spill 58
+// Not near a copy: rows of 8193 to 12288 values held in 64 bits, which spill 58
 // registers (16384 x 11008 with a norm of the branch: 701 us, 1.8 TB/s), and
 // operands that are not 4-aligned, value by value (8192 x 4097: 151 us, 48 for
 // 4096).
