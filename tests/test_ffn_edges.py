@@ -114,3 +114,12 @@ def test_weights_tensors_cannot_be_replaced(on_host, name):
     with pytest.raises(AttributeError):
         setattr(w, name, 2 * held)
     assert getattr(w, name) is held and held.data_ptr() in w._c
+
+
+@pytest.mark.parametrize("E,N", [(2, 5), (4, 1)])
+def test_biases_that_experts_share(on_host, E, N):
+    """Laid out for each expert, as scales are; the C call refuses a stride of 0."""
+    row = torch.arange(1.0, N + 1)
+    w = on_host.ExpertWeights(torch.zeros(E, N, 4, dtype=torch.int32), 100, alpha=torch.ones(E), bias=row.expand(E, N))
+    address, stride = w._c[3:5]
+    assert stride >= N and address == w.bias.data_ptr() and torch.equal(w.bias, row.expand(E, N))

@@ -1196,10 +1196,10 @@ class ExpertWeights:
 
     ``Wp``, ``Zp``: the planes of pack_weights (``Zp`` None) or
     pack_weights_ternary, [N, ld] of a single layer or [experts, N, ld]
-    stacked.  ``alpha`` float32 [experts, N] ([N] of a single layer; a row
-    that experts share, as by ``expand``, is copied for each), or [experts]
-    with one scale for a whole matrix; ``bias`` float32 like [experts, N], or
-    None.  The planes are not needed afterwards; ``alpha`` and ``bias`` are
+    stacked.  ``alpha`` float32 [experts, N] ([N] of a single layer), or
+    [experts] with one scale for a whole matrix; ``bias`` float32 like
+    [experts, N], or None.  A row of either that experts share, as by
+    ``expand``, is copied for each.  The planes are not needed afterwards; ``alpha`` and ``bias`` are
     kept and read by each call."""
 
     def __init__(self, Wp: torch.Tensor, K: int, *, Zp: torch.Tensor | None = None, alpha: torch.Tensor, bias: torch.Tensor | None = None):
@@ -1228,14 +1228,18 @@ class ExpertWeights:
         if alpha.shape == (self.experts,):
             scale = _vector(alpha, torch.float32, "alpha", self.experts, index), 0
         else:
-            if alpha.dim() == 2 and self.experts > 1 and alpha.stride(0) < self.N:
-                alpha = alpha.contiguous()   # a row that experts share: a stride of 0 would say that each has a single scale
+            alpha = self._rows(alpha)
             scale = _matrix(alpha, torch.float32, "alpha", self.experts, self.N, index)
         shift = 0, 0
         if bias is not None:
+            bias = self._rows(_dev(bias, torch.float32, "bias"))
             shift = _matrix(bias[None] if bias.dim() == 1 else bias, torch.float32, "bias", self.experts, self.N, index)
         self._held = W, alpha, bias
         self._c = (W.data_ptr() or _EMPTY, *scale, *shift)
+
+    def _rows(self, t: torch.Tensor) -> torch.Tensor:
+        """A row that experts share laid out for each: a stride of 0 says that each has a single scale, and no bias can have it."""
+        return t.contiguous() if t.dim() == 2 and self.experts > 1 and t.stride(0) < self.N else t
 
     # Their addresses are in _c: they can be written in place, not replaced.
     W = property(lambda self: self._held[0])
